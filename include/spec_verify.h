@@ -418,6 +418,74 @@ SPEC_API int spec_lm_head_argmax(spec_ctx* ctx, const void* w_head_tiled,
 SPEC_API int spec_attention(spec_ctx* ctx, const spec_kv* kv, int layer,
                    const float* q, int M, float* out);
 
+/* The same attention with an optional window and sinks, over the paged bf16
+ * cache: row i, at position p = seq_len - M + i, sees the positions t <= p with
+ * t > p - window or t < sinks (the first positions that stay visible: a draft's
+ * cheap view of a long context).  window = 0: every t <= p, sinks ignored.
+ * 1 <= M <= 16; window, sinks >= 0.  A key on an unmapped page is not seen; a
+ * row that sees no key (seq_len < M) is zero.  What a row does not see does not
+ * reach it, NaN and infinities included.  Row i's result is the same bits for
+ * every M that places it at the same position.  A layer that is a sliding-window layer of the
+ * ctx keeps its K/V in a ring, not in the pool, and is refused (SPEC_EINVAL).
+ * q DEVICE fp32 [M][n_q_heads][head_dim]; out DEVICE fp32
+ * [M][n_q_heads*head_dim]; both 16-byte aligned, not overlapping. */
+SPEC_API int spec_attention_window(spec_ctx* ctx, const spec_kv* kv, int layer, const float* q, int M,
+                                   int window, int sinks, float* out);
+
+/* ---- QK-norm and rotary embedding as a building block: what the verify step
+ * does to the q and k heads between the QKV GEMM and the cache, for n rows.
+ *   x    DEVICE fp32 [n][ldx]: each row's first (n_q_heads + n_kv_heads) *
+ *        head_dim columns are its q heads, then its k heads (the QKV GEMM's
+ *        layout; the V columns behind them are not touched)
+ *   pos  DEVICE int32 [n]: positions of the rows; read only when the ctx has
+ *        rope_theta > 0 (NULL otherwise).  A position outside [0, max_ctx) sets
+ *        SPEC_ST_CTX_FULL in the ctx status word and gives a zero row.
+ *   q_norm, k_norm  DEVICE fp32 [head_dim] gains, or NULL: no norm of that side
+ *   out  DEVICE fp32 [n][ldo], the same columns; out = x with ldo = ldx is
+ *        allowed, any other overlap refused (SPEC_EINVAL)
+ * Every head is normalised, x * g / sqrt(mean(x^2) + rms_eps), then rotated as
+ * spec_config.rope_theta says.  ldx, ldo multiples of 4; n >= 0. */
+SPEC_API int spec_qk_norm_rope(spec_ctx* ctx, const float* x, int ldx, int n, const int32_t* pos,
+                               const float* q_norm, const float* k_norm, float* out, int ldo);
+
+/* ---- 4-bit KV cache.  A spec_kv whose pool holds 4-bit pages:
+ *   pool  uint8 [num_pages][n_layers][2 (K,V)][n_kv_heads][SPEC_KV4_PAGE_BYTES]
+ * with the page table, length and free stack of any other cache, so
+ * spec_kv_reset, spec_kv_extend and spec_kv_rollback serve it as they are.
+ * Every layer has its pages (the rings of sliding-window layers hold bf16
+ * rows and are not used here).  A page holds 16 positions of one head:
+ *   byte 256*c + 16*t + j  codes of elements 32c+2j (low nibble) and 32c+2j+1
+ *                          of position t (c < 4, j < 16)
+ *   byte 1024 + 8*t + g    scale of elements 16g..16g+15 of position t
+ * A code is e2m1 (bit 3 the sign; 0, .5, 1, 1.5, 2, 3, 4, 6); a scale byte b is
+ * the binary16 number of bits b << 7, and bytes above 0xE2 (10240) read as
+ * 0xE2.  Value = code * scale, exact in fp32, bf16 and binary16: 4.5 bits per
+ * value against bf16's 16. */
+#define SPEC_KV4_PAGE_BYTES 1152
+
+/* Quantise n rows of K and V into the pages of positions seq_len-n..seq_len-1
+ * (mapped by spec_kv_extend before).  k, v DEVICE fp32 [n][ld], the row's
+ * n_kv_heads*head_dim values first (columns of a QKV GEMM's output with its
+ * row stride, for instance); 16-byte aligned, ld a multiple of 4, n >= 0.
+ * Per group of 16: the smallest scale s with 6 s >= the largest magnitude
+ * (10240 if none), then the code nearest to x / s, ties to the even code; both
+ * decided exactly.  A larger magnitude saturates at 61440.  A NaN is stored as
+ * 0, an infinity as 61440 of its sign, and both set SPEC_ST_NONFINITE in the
+ * ctx status word.  A row whose position is negative or on an unmapped page is
+ * left out and sets SPEC_ST_CTX_FULL. */
+SPEC_API int spec_kv4_append(spec_ctx* ctx, const spec_kv* kv, int layer, const float* k, const float* v,
+                             int ld, int n);
+
+/* The values of positions pos0..pos0+n-1 as fp32 rows: k, v DEVICE fp32
+ * [n][ld], n_kv_heads*head_dim columns written.  A position at or past seq_len
+ * or on an unmapped page reads as zeros.  pos0, n >= 0. */
+SPEC_API int spec_kv4_read(spec_ctx* ctx, const spec_kv* kv, int layer, int pos0, int n, float* k,
+                           float* v, int ld);
+
+/* spec_attention_window over a 4-bit cache (any layer). */
+SPEC_API int spec_attention_kv4(spec_ctx* ctx, const spec_kv* kv, int layer, const float* q, int M,
+                                int window, int sinks, float* out);
+
 /* Greedy accept + rollback alone (the last kernel of a step).
  *   idx    DEVICE int32 [k+1] per-row argmax of rows 0..k
  *   draft  DEVICE int32 [k]

@@ -76,6 +76,11 @@ _SIGS = {
     "spec_gemm_wait_selftest": (I, [P, P, I, I]),
     "spec_lm_head_argmax": (I, [P, P, P, P, I, P, P]),
     "spec_attention": (I, [P, C.POINTER(spec_kv), I, P, I, P]),
+    "spec_attention_window": (I, [P, C.POINTER(spec_kv), I, P, I, I, I, P]),
+    "spec_qk_norm_rope": (I, [P, P, I, I, P, P, P, P, I]),
+    "spec_kv4_append": (I, [P, C.POINTER(spec_kv), I, P, P, I, I]),
+    "spec_kv4_read": (I, [P, C.POINTER(spec_kv), I, I, I, P, P, I]),
+    "spec_attention_kv4": (I, [P, C.POINTER(spec_kv), I, P, I, I, I, P]),
     "spec_accept": (I, [P, P, P, I, C.POINTER(spec_kv), P]),
     "spec_profile_gemms": (I, [P, I]),
     "spec_profile_read": (I, [P, C.POINTER(C.c_float), C.POINTER(C.c_int)]),
@@ -92,6 +97,7 @@ _SIGS = {
 }
 
 MT_WORDS = 625
+KV4_PAGE_BYTES = 1152      # 16 positions of one head of a 4-bit cache
 
 _lib = None
 
@@ -211,6 +217,26 @@ def spec_lm_head_argmax(ctx, w_head, final_norm, x, M, idx, logits) -> int:
 
 def spec_attention(ctx, kv, layer, q, M, out) -> int:
     return _call("spec_attention", ctx, C.byref(kv), layer, P(q), M, P(out))
+
+
+def spec_attention_window(ctx, kv, layer, q, M, window, sinks, out) -> int:
+    return _call("spec_attention_window", ctx, C.byref(kv), layer, P(q), M, window, sinks, P(out))
+
+
+def spec_attention_kv4(ctx, kv, layer, q, M, window, sinks, out) -> int:
+    return _call("spec_attention_kv4", ctx, C.byref(kv), layer, P(q), M, window, sinks, P(out))
+
+
+def spec_qk_norm_rope(ctx, x, ldx, n, pos, q_norm, k_norm, out, ldo) -> int:
+    return _call("spec_qk_norm_rope", ctx, P(x), ldx, n, P(pos), P(q_norm), P(k_norm), P(out), ldo)
+
+
+def spec_kv4_append(ctx, kv, layer, k, v, ld, n) -> int:
+    return _call("spec_kv4_append", ctx, C.byref(kv), layer, P(k), P(v), ld, n)
+
+
+def spec_kv4_read(ctx, kv, layer, pos0, n, k, v, ld) -> int:
+    return _call("spec_kv4_read", ctx, C.byref(kv), layer, pos0, n, P(k), P(v), ld)
 
 
 def spec_verify_tree(ctx, w, kv, hidden, tokens, parent, n, res, path_out, taps: spec_taps | None) -> int:

@@ -481,6 +481,94 @@ int spec_attention(spec_ctx* c, const spec_kv* kv, int layer, const float* q, in
   return SPEC_OK;
 }
 
+// [a, a + na) and [b, b + nb) share a byte
+static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+// bytes from the first to the last value of n rows of w fp32 columns, stride ld
+static size_t span_bytes(int n, int ld, int w) { return n > 0 ? 4 * ((size_t)(n - 1) * ld + w) : 0; }
+
+// rows of w columns at a and at b, both of stride ld, fall between one another
+// (K and V columns of one matrix)
+static bool rows_interleave(const float* a, const float* b, int ld, int w) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  const size_t off = (x < y ? y - x : x - y) / 4 % ld;
+  return off >= (size_t)w && off + w <= (size_t)ld;
+}
+
+static int paged_attention(spec_ctx* c, bool k4, const spec_kv* kv, int layer, const float* q, int M, int window,
+                           int sinks, float* out) {
+  if (!c || !q || !out) return SPEC_ENULL;
+  int rc = check_kv(kv);
+  if (rc) return rc;
+  if (M < 1 || M > 16 || layer < 0 || layer >= c->cfg.n_layers || window < 0 || sinks < 0) return SPEC_EINVAL;
+  const KvView v = view_of(c, kv);
+  if (!k4 && swa_index(v, layer) >= 0) return SPEC_EINVAL;   // its K/V are in a ring
+  if (!aligned(q) || !aligned(out)) return SPEC_EALIGN;
+  const size_t bytes = span_bytes(M, c->cfg.n_q_heads * 128, c->cfg.n_q_heads * 128);
+  if (overlap(q, bytes, out, bytes)) return SPEC_EINVAL;
+  return cuda_code(launch_paged_attention(k4, v, layer, q, M, c->cfg.n_q_heads, window, sinks, out, c->stream));
+}
+
+int spec_attention_window(spec_ctx* c, const spec_kv* kv, int layer, const float* q, int M, int window, int sinks,
+                          float* out) {
+  return paged_attention(c, false, kv, layer, q, M, window, sinks, out);
+}
+
+int spec_attention_kv4(spec_ctx* c, const spec_kv* kv, int layer, const float* q, int M, int window, int sinks,
+                       float* out) {
+  return paged_attention(c, true, kv, layer, q, M, window, sinks, out);
+}
+
+int spec_qk_norm_rope(spec_ctx* c, const float* x, int ldx, int n, const int32_t* pos, const float* q_norm,
+                      const float* k_norm, float* out, int ldo) {
+  if (!c || !x || !out) return SPEC_ENULL;
+  const int w = (c->cfg.n_q_heads + c->cfg.n_kv_heads) * c->cfg.head_dim;
+  if (n < 0 || ldx < w || ldo < w || ldx % 4 || ldo % 4) return SPEC_EINVAL;
+  if (c->rope_cs && !pos) return SPEC_ENULL;
+  if (!aligned(x) || !aligned(out) || (q_norm && !aligned(q_norm)) || (k_norm && !aligned(k_norm))) return SPEC_EALIGN;
+  if (!(x == out && ldx == ldo) && overlap(x, span_bytes(n, ldx, w), out, span_bytes(n, ldo, w))) return SPEC_EINVAL;
+  if (n == 0) return SPEC_OK;
+  QkTransform t;
+  t.gq = q_norm;
+  t.gk = k_norm;
+  t.cs = c->rope_cs;
+  t.cs_len = c->cfg.max_ctx;
+  t.eps = c->cfg.rms_eps;
+  return cuda_code(launch_qk_norm_rope(x, ldx, n, c->cfg.n_q_heads, c->cfg.n_kv_heads, pos, t, out, ldo, c->status,
+                                       c->stream));
+}
+
+// the checks that the two row transfers of a 4-bit cache share
+static int check_kv4_rows(spec_ctx* c, const spec_kv* kv, int layer, const float* k, const float* v, int ld, int n) {
+  if (!c || !k || !v) return SPEC_ENULL;
+  int rc = check_kv(kv);
+  if (rc) return rc;
+  if (layer < 0 || layer >= c->cfg.n_layers || n < 0) return SPEC_EINVAL;
+  if (ld < c->cfg.n_kv_heads * c->cfg.head_dim || ld % 4) return SPEC_EINVAL;
+  if (!aligned(k) || !aligned(v)) return SPEC_EALIGN;
+  return SPEC_OK;
+}
+
+int spec_kv4_append(spec_ctx* c, const spec_kv* kv, int layer, const float* k, const float* v, int ld, int n) {
+  int rc = check_kv4_rows(c, kv, layer, k, v, ld, n);
+  if (rc || n == 0) return rc;
+  return cuda_code(launch_kv4_append(k, v, ld, n, view_of(c, kv), layer, c->status, c->stream));
+}
+
+int spec_kv4_read(spec_ctx* c, const spec_kv* kv, int layer, int pos0, int n, float* k, float* v, int ld) {
+  int rc = check_kv4_rows(c, kv, layer, k, v, ld, n);
+  if (rc) return rc;
+  if (pos0 < 0 || pos0 > INT32_MAX - n) return SPEC_EINVAL;
+  const size_t bytes = span_bytes(n, ld, c->cfg.n_kv_heads * c->cfg.head_dim);
+  if (k == v || (overlap(k, bytes, v, bytes) && n > 0 &&
+                 !rows_interleave(k, v, ld, c->cfg.n_kv_heads * c->cfg.head_dim)))
+    return SPEC_EINVAL;
+  if (n == 0) return SPEC_OK;
+  return cuda_code(launch_kv4_read(view_of(c, kv), layer, pos0, n, k, v, ld, c->stream));
+}
+
 int spec_accept(spec_ctx* c, const int32_t* idx, const int32_t* draft, int k, spec_kv* kv,
                 spec_result* res) {
   if (!c || !idx || !draft || !res) return SPEC_ENULL;

@@ -120,6 +120,20 @@ cudaError_t launch_attention(const AttnPlan& a, const KvView& kv, int layer, con
                              cudaStream_t st, bool pdl, const uint64_t* tree_mask = nullptr,
                              const int32_t* tree_base = nullptr);
 
+// QK-norm and RoPE of the q and k heads (the first nq + nkv heads of each row)
+cudaError_t launch_qk_norm_rope(const float* x, int ldx, int n, int nq, int nkv, const int32_t* pos,
+                                const QkTransform& t, float* out, int ldo, int32_t* status, cudaStream_t st);
+
+// 4-bit cache (KvView::pool holds 4-bit pages): rows in, rows out
+cudaError_t launch_kv4_append(const float* k, const float* v, int ld, int n, const KvView& kv, int layer,
+                              int32_t* status, cudaStream_t st);
+cudaError_t launch_kv4_read(const KvView& kv, int layer, int pos0, int n, float* k, float* v, int ld,
+                            cudaStream_t st);
+// attention of M rows over a paged cache (k4: 4-bit pages, else bf16) with an
+// optional window (0: none) and sinks
+cudaError_t launch_paged_attention(bool k4, const KvView& kv, int layer, const float* q, int M, int nq, int window,
+                                   int sinks, float* out, cudaStream_t st);
+
 // stochastic exact acceptance: row normalizers (stats fp32x2 [k+1]: max and
 // sum of exp) then the decisions, the final draw and the rollback; mt is the
 // 625-word MT19937 state (DEVICE), advanced by the draws

@@ -130,6 +130,10 @@ class DeviceKV:
         self.cfg = cfg
         self.pool = torch.zeros((num_pages, cfg.n_layers, 2, cfg.n_kv_heads, cfg.page_size,
                                  cfg.head_dim), dtype=torch.bfloat16, device="cuda")
+        self._init_metadata(num_pages, max_seq_pages)
+
+    def _init_metadata(self, num_pages: int, max_seq_pages: int):
+        cfg = self.cfg
         self.page_table = torch.full((max_seq_pages,), -1, dtype=torch.int32, device="cuda")
         self.seq_len = torch.zeros(4, dtype=torch.int32, device="cuda")
         self.free_stack = torch.zeros(num_pages, dtype=torch.int32, device="cuda")
@@ -212,3 +216,28 @@ class DeviceKV:
             page = int(pt[lp])
             pool16[page, layer, 0, :, : b - a, :] = kb[a:b].permute(1, 0, 2)
             pool16[page, layer, 1, :, : b - a, :] = vb[a:b].permute(1, 0, 2)
+
+
+class DeviceKV4(DeviceKV):
+    """Paged 4-bit KV cache: the same metadata, pages of abi.KV4_PAGE_BYTES bytes
+    (spec_kv4_append writes them, spec_attention_kv4 reads them)."""
+
+    def __init__(self, cfg: ModelConfig, num_pages: int, max_seq_pages: int):
+        self.cfg = cfg
+        self.pool = torch.zeros((num_pages, cfg.n_layers, 2, cfg.n_kv_heads, abi.KV4_PAGE_BYTES),
+                                dtype=torch.uint8, device="cuda")
+        self._init_metadata(num_pages, max_seq_pages)
+
+    def append(self, ctx: Context, layer: int, k: torch.Tensor, v: torch.Tensor):
+        """Quantise fp32 rows [n][n_kv*dh] (row stride shared by k and v) into
+        the last n positions, which extend() has mapped."""
+        assert k.stride(0) == v.stride(0) and k.shape == v.shape and k.stride(1) == v.stride(1) == 1
+        abi.check("spec_kv4_append", abi.spec_kv4_append(ctx.h, self.struct(), layer, ptr(k), ptr(v), k.stride(0),
+                                                         k.shape[0]))
+
+    def read(self, ctx: Context, layer: int, pos0: int, n: int):
+        """fp32 (k, v) rows [n][n_kv*dh] of positions pos0 .. pos0+n-1."""
+        w = self.cfg.n_kv_heads * self.cfg.head_dim
+        k, v = torch.empty((n, w), device="cuda"), torch.empty((n, w), device="cuda")
+        abi.check("spec_kv4_read", abi.spec_kv4_read(ctx.h, self.struct(), layer, pos0, n, ptr(k), ptr(v), w))
+        return k, v
