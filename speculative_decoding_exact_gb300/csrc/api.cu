@@ -249,6 +249,8 @@ int spec_verify_init(const spec_config* cfg, void* cuda_stream, spec_ctx** out) 
   {
     size_t parts = attn_partial_floats(c->attn, 16);
     if (has_swa(*cfg) && attn_partial_floats(c->attn_swa, 16) > parts) parts = attn_partial_floats(c->attn_swa, 16);
+    const size_t paged = paged_attention_floats(cfg->n_q_heads, cfg->n_kv_heads, 16, sms);
+    if (paged > parts) parts = paged;
     rc |= dalloc(&c->attn_part, parts);
   }
   rc |= dalloc(&c->head_val, (size_t)c->head_parts * 16);
@@ -508,7 +510,8 @@ static int paged_attention(spec_ctx* c, bool k4, const spec_kv* kv, int layer, c
   if (!aligned(q) || !aligned(out)) return SPEC_EALIGN;
   const size_t bytes = span_bytes(M, c->cfg.n_q_heads * 128, c->cfg.n_q_heads * 128);
   if (overlap(q, bytes, out, bytes)) return SPEC_EINVAL;
-  return cuda_code(launch_paged_attention(k4, v, layer, q, M, c->cfg.n_q_heads, window, sinks, out, c->stream));
+  return cuda_code(launch_paged_attention(k4, v, layer, q, M, c->cfg.n_q_heads, window, sinks, c->num_sms, c->attn_part,
+                                          out, c->status, c->stream));
 }
 
 int spec_attention_window(spec_ctx* c, const spec_kv* kv, int layer, const float* q, int M, int window, int sinks,

@@ -22,8 +22,7 @@
 // Precision: K and V are exact bf16; q and p are split into bf16 hi + lo parts
 // (two MMAs each) so the products carry ~16 significant bits; accumulation is
 // fp32.
-#include <cuda.h>
-
+#include "attn_mma.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "quant.cuh"
@@ -117,20 +116,11 @@ size_t attn_partial_floats(const AttnPlan& a, int max_rows) {
   return (size_t)a.max_chunks * a.nq * 16 * kPartStride;
 }
 
-// 2-D tensor copy global -> shared: box at (x, y) of the map, completion on mbar
-SPEC_DEV void tma_load_2d(void* dst_smem, const CUtensorMap* map, int x, int y, uint64_t* mbar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
-          smem_u32(dst_smem)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(mbar))
-      : "memory");
-}
-
 // The KV pool [num_pages][n_layers][K, V][n_kv][16 positions][128] bf16 seen as
 // one 2-D tensor of 256-byte rows (row = ((page*n_layers + layer)*2 + kv)*n_kv
 // + head, times 16, plus the position in the page); boxes of 16 rows x 64
 // values (one d half of one page), 128-byte swizzle.
-static cudaError_t make_kv_tmap(const KvView& kv, CUtensorMap* map) {
+cudaError_t make_kv_tmap(const KvView& kv, CUtensorMap* map) {
   using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -183,12 +173,6 @@ static cudaError_t make_ring_tmap(const KvView& kv, CUtensorMap* map) {
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// 2^x (PTX ex2.approx: relative error about 2^-22; 2^-inf = 0)
-SPEC_DEV float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
 // split x into bf16 hi + bf16 lo, packed pairs (x0 in the low half): hi is x
 // with the low 16 bits dropped (exact), lo = x - hi (exact in fp32, below
 // 2^-7 |x|) rounded to bf16, so hi + lo carries about 16 significant bits
@@ -205,20 +189,6 @@ SPEC_DEV void tmem_st16(uint32_t taddr, const uint32_t* r) {
           taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
-}
-SPEC_DEV void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-// shared-memory descriptor of a 128-byte-swizzled operand: lbo and sbo in bytes
-SPEC_DEV uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return smem_desc(saddr, lbo, sbo) | ((uint64_t)2 << 61);
 }
 // D[tmem] (+)= A[smem] * B[smem]^T, kind::f16, issued by one thread
 SPEC_DEV void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {

@@ -132,7 +132,8 @@ cudaError_t launch_kv4_read(const KvView& kv, int layer, int pos0, int n, float*
 // attention of M rows over a paged cache (k4: 4-bit pages, else bf16) with an
 // optional window (0: none) and sinks
 cudaError_t launch_paged_attention(bool k4, const KvView& kv, int layer, const float* q, int M, int nq, int window,
-                                   int sinks, float* out, cudaStream_t st);
+                                   int sinks, int num_sms, float* part, float* out, int32_t* status, cudaStream_t st);
+size_t paged_attention_floats(int nq, int nkv, int max_rows, int num_sms);   // floats of `part`
 
 // stochastic exact acceptance: row normalizers (stats fp32x2 [k+1]: max and
 // sum of exp) then the decisions, the final draw and the rollback; mt is the
