@@ -22,6 +22,8 @@
 // Precision: K and V are exact bf16; q and p are split into bf16 hi + lo parts
 // (two MMAs each) so the products carry ~16 significant bits; accumulation is
 // fp32.
+#include <cuda.h>
+
 #include "attn_mma.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -116,11 +118,20 @@ size_t attn_partial_floats(const AttnPlan& a, int max_rows) {
   return (size_t)a.max_chunks * a.nq * 16 * kPartStride;
 }
 
+// 2-D tensor copy global -> shared: box at (x, y) of the map, completion on mbar
+SPEC_DEV void tma_load_2d(void* dst_smem, const CUtensorMap* map, int x, int y, uint64_t* mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
+          smem_u32(dst_smem)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(mbar))
+      : "memory");
+}
+
 // The KV pool [num_pages][n_layers][K, V][n_kv][16 positions][128] bf16 seen as
 // one 2-D tensor of 256-byte rows (row = ((page*n_layers + layer)*2 + kv)*n_kv
 // + head, times 16, plus the position in the page); boxes of 16 rows x 64
 // values (one d half of one page), 128-byte swizzle.
-cudaError_t make_kv_tmap(const KvView& kv, CUtensorMap* map) {
+static cudaError_t make_kv_tmap(const KvView& kv, CUtensorMap* map) {
   using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -189,13 +200,6 @@ SPEC_DEV void tmem_st16(uint32_t taddr, const uint32_t* r) {
           taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
-}
-// D[tmem] (+)= A[smem] * B[smem]^T, kind::f16, issued by one thread
-SPEC_DEV void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
 }
 // bulk copy shared -> global (bulk group of this thread)
 SPEC_DEV void bulk_s2g(void* dst, const void* src_smem, uint32_t bytes) {

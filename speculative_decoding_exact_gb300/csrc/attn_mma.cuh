@@ -1,21 +1,9 @@
-// attn_mma.cuh — what the attention kernels share: tensor copies, tensor-memory
-// loads, operand descriptors and the base-2 exponential.
+// attn_mma.cuh — what the attention kernels share: tensor-memory loads, operand
+// descriptors, the shared-memory MMA and the base-2 exponential.
 #pragma once
-#include <cuda.h>
-
 #include "common.cuh"
-#include "internal.h"
 
 namespace spec {
-
-// 2-D tensor copy global -> shared: box at (x, y) of the map, completion on mbar
-SPEC_DEV void tma_load_2d(void* dst_smem, const CUtensorMap* map, int x, int y, uint64_t* mbar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
-          smem_u32(dst_smem)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(mbar))
-      : "memory");
-}
 
 // 2^x (PTX ex2.approx: relative error about 2^-22; 2^-inf = 0)
 SPEC_DEV float exp2_approx(float x) {
@@ -37,7 +25,12 @@ SPEC_DEV void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
 SPEC_DEV uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
   return smem_desc(saddr, lbo, sbo) | ((uint64_t)2 << 61);
 }
-// the tensor map of a bf16 KV pool (defined in attn.cu)
-cudaError_t make_kv_tmap(const KvView& kv, CUtensorMap* map);
+// D[tmem] (+)= A[smem] * B[smem]^T, kind::f16, issued by one thread
+SPEC_DEV void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
 
 }  // namespace spec
