@@ -65,11 +65,10 @@ def visible(M, length, window, sinks, mapped=None):
 
 
 # Error bound of the attention kernels, relative per weight.  With eps = 2^-24:
-#  - a value is split into two operand parts, each rounded to nearest with p
-#    significant bits: off by 2^-2p relative (bf16, p = 8: 2^-16 bounds the
-#    2^-18 of two half steps with margin for cancellation at the part border;
-#    binary16, p = 11: 2^-22), plus 2^-31 of a row's largest weight where
-#    binary16 leaves its normal range;
+#  - q and p are split into two binary16 parts, each rounded to nearest with 11
+#    significant bits: off by at most half a step of the second, 2^-22 relative
+#    (`split`), plus 2^-31 of a row's largest weight where binary16 leaves its
+#    normal range;
 #  - the score is a sum of 256 products (two parts), each add off by at most
 #    2 eps (the tensor core may truncate): 512 eps of sum |q k|; scaled by
 #    log2(e) / sqrt(128) (3 eps) and subtracted from the maximum, exp2 is off by
@@ -89,7 +88,7 @@ def attention_bound(q, k, v, w, see, split):
     return rel * mean + n * 2.0 ** -31 * np.abs(np.where(see.any(0)[:, None], v, 0)).max() + 1e-30
 
 
-def attention(q, k, v, nq, window, sinks, length, mapped=None, split=2.0 ** -16):
+def attention(q, k, v, nq, window, sinks, length, mapped=None, split=2.0 ** -22):
     """q [M][nq][128], k, v float64 [>= length][nkv][128] -> (o, bound) [M][nq*128]."""
     M, nkv = q.shape[0], k.shape[1]
     see = visible(M, length, window, sinks, mapped)

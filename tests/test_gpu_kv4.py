@@ -101,8 +101,9 @@ def attend(ctx, kv, kind, q, window, sinks, layer=1):
     return out.cpu().numpy()
 
 
-# a row's largest weight is 2^0 .. 2^8 of its reference: kv4_util's split terms
-SPLIT = {"kv4": 2.0 ** -22, "bf16": 2.0 ** -16}
+# what q, p and the values lose as MMA operands (kv4_util): two binary16 parts,
+# and for bf16 values below 2^-17, of which these inputs have some, 2^-25 each
+SPLIT = {"kv4": 2.0 ** -22, "bf16": 2.0 ** -21}
 
 
 def check_attention(ctx, kind, M, length, window, sinks, seed=0, spread=1.0, q_scale=1.0):
@@ -393,6 +394,30 @@ def test_attention_is_untouched_by_what_rows_do_not_see(kind, window, sinks):
                 elif math.isnan(val):
                     assert not np.isfinite(g).any()
                 kv.pool.copy_(saved)
+
+
+@pytest.mark.parametrize("M,window,sinks", [(1, 0, 0), (16, 0, 0), (16, 100, 5), (5, 40, 200)])
+def test_attention_bf16_values_past_binary16(M, window, sinks):
+    """bf16 elements from 2^15 up to the type's largest, and whole tiny rows:
+    what binary16 operands cannot hold is worked on in fp32."""
+    ctx = context(26, 2)
+    length = 400
+    kv, k, v, ids = cache(ctx, "bf16", length, 71)
+    rng = np.random.default_rng(9)
+    q = rng.standard_normal((M, 26, 128)).astype(np.float32)
+    for n, (t, which, d, val) in enumerate([(3, 1, 5, 40000.0), (3, 1, 6, -1e9), (200, 1, 0, 32768.0), (390, 1, 127, 7e4),
+                                            (length - 1, 1, 64, 1e30), (130, 0, 9, 70000.0), (length - 2, 0, 8, -1e5),
+                                            (131, 0, slice(None), 1e-7), (132, 1, slice(None), 1e-7),
+                                            (300, 1, slice(None), -65536.0)]):
+        x = torch.full((2, 128), val).bfloat16() if isinstance(d, slice) else torch.tensor(val).bfloat16()
+        kv.pool[int(ids[t // 16]), 1, which, :, t % 16, d] = x.cuda()
+        (k, v)[which][t, :, d] = x.double().numpy()
+    q[:, :, 8:10] *= 1e-4          # so that the large K elements do not decide every row
+    sync()
+    got = attend(ctx, kv, "bf16", q, window, sinks)
+    want, bound = u.attention(q, k, v, 26, window, sinks, length, split=SPLIT["bf16"])
+    assert (np.abs(got - want) <= bound).all(), float((np.abs(got - want) / bound).max())
+    assert status(ctx) == 0
 
 
 @pytest.mark.parametrize("kind", KINDS)
