@@ -424,9 +424,13 @@ SPEC_API int spec_attention(spec_ctx* ctx, const spec_kv* kv, int layer,
  * cheap view of a long context).  window = 0: every t <= p, sinks ignored.
  * 1 <= M <= 16; window, sinks >= 0.  A key on an unmapped page is not seen; a
  * row that sees no key (seq_len < M) is zero.  What a row does not see does not
- * reach it, NaN and infinities included.  Row i's result is the same bits for
- * every M that places it at the same position.  A layer that is a sliding-window layer of the
- * ctx keeps its K/V in a ring, not in the pool, and is refused (SPEC_EINVAL).
+ * reach it, NaN and infinities included.  With r = M * n_q_heads / n_kv_heads
+ * the query rows of a KV head, calls are of one kind for r <= 16 and of another
+ * for every value of ceil(r / 128) above; row i's result is the same bits in
+ * every call of a kind that places it at the same position, and differs by
+ * rounding between kinds (a token alone and inside a verify block, say).  A
+ * layer that is a sliding-window layer of the ctx keeps its K/V in a ring, not
+ * in the pool, and is refused (SPEC_EINVAL).
  * q DEVICE fp32 [M][n_q_heads][head_dim]; out DEVICE fp32
  * [M][n_q_heads*head_dim]; both 16-byte aligned, not overlapping. */
 SPEC_API int spec_attention_window(spec_ctx* ctx, const spec_kv* kv, int layer, const float* q, int M,

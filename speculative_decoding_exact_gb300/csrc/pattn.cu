@@ -5,10 +5,11 @@
 // t > p - window or t < sinks (window 0: every t <= p).
 // s_t = q.k_t / sqrt(128), o = sum_t exp(s_t - m) v_t / sum_t exp(s_t - m).
 //
+// Calls with at most 16 query rows per KV head go to pattn_few.cu.
+//
 // Decomposition (flash-decoding).  The M * group query rows of a KV head (group
 // query heads read it) are packed into tiles of up to 128 rows, the rows of the
-// tcgen05 MMAs, so that one decoded token of 13 heads and a block of 104 rows
-// both take one tile.  Keys are taken in tiles of 128 at absolute positions:
+// tcgen05 MMAs.  Keys are taken in tiles of 128 at absolute positions:
 //   S[128 x 128 keys] = Q[128 x 128 d] . K^T      (A = Q in TMEM, B = K)
 //   O[128 x 128 d]    = P[128 x 128 keys] . V     (A = P in TMEM, B = V)
 // with a running (max, sum) per row.  A CTA (slot, KV head, row tile) walks one
@@ -16,18 +17,17 @@
 // Q and P live in TMEM because shared memory is the busiest unit: a tile's K
 // and V are written once and read twice, 192 KB.  With the keys on the MMA's
 // rows and Q and P in shared memory (a tile's work then follows the number of
-// query rows) 52 rows cost as much as 128 do here: 113 against 24 us for 208
-// rows over 32k keys, and one token behind 128k keys was no faster.
+// query rows), 208 rows over 32k keys took 100 us instead of 57.
 //
-// The split of the keys is a function of the row's own position alone (chunk_len
-// below): chunks are whole multiples of L tiles from position 0, so a row has
-// the same bits alone and in any block (batch-height invariance).  L grows
-// with the position such that there are never more chunks than SMs per KV head;
-// a block that crosses such a step runs its two groups of rows one after the
+// The split of the keys is a function of the row's own position and the number of
+// row tiles (chunk_len, pattn_plan.cuh): chunks are whole multiples of L tiles
+// from position 0, so a row has the same bits in every block of as many row tiles
+// (batch-height invariance).  L grows with the position such that there are never
+// more chunks than SMs per KV head and row tile; a block that crosses such a step runs its two groups of rows one after the
 // other.  Tiles that no row sees are skipped: they would add exact zeros.
 //
 // Precision: all operands are binary16.  A 4-bit value is exact in it; a bf16
-// value is exact when 2^-17 <= |x| < 2^15 (below: off by at most 2^-25 absolute;
+// value is exact when 2^-17 <= |x| < 2^16 (below: off by at most 2^-25 absolute;
 // larger and non-finite elements are worked on in fp32, see `odd` below).  q and
 // p are split into two parts, 22 significant bits.  The tensor core truncates
 // its additions, so the small parts go first, and each tile's O starts afresh
@@ -37,11 +37,10 @@
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.cuh"
+#include "pattn_plan.cuh"
 
 namespace spec {
 
-constexpr int kKeys = 128;                          // keys of a tile
-constexpr int kPagesPerTile = kKeys / 16;
 constexpr int kHalf = kKeys * 128;                  // one d half of a K or V tile: [keys][64 values]
 constexpr int kStageBytes = 4 * kHalf;              // K then V, 64 KB
 constexpr uint64_t kPattnWaitNs = 2000000000ull;
@@ -61,70 +60,6 @@ constexpr int kTmAll = 512;
 // and the others 80 (96).
 constexpr int kSoftWarps = 8, kWQk = 8, kWPv = 9, kWLoad = 10, kUnpackWarps = 6;
 constexpr int kPattnThreads = 512;
-
-struct PattnPlan {
-  int M, nq, nkv, group, window, sinks;
-  int C;                     // chunks of a KV head at most
-  int slots;                 // chunk slots launched (<= C)
-  int Lw;                    // tiles per chunk at most (what the window needs)
-  int tile_rows;             // rows per row tile
-};
-
-// tiles per chunk of a row at position p
-SPEC_DEV int chunk_len(const PattnPlan& pl, int p) {
-  const int l = p > 0 ? (p >> 7) / pl.C + 1 : 1;
-  return l < pl.Lw ? l : pl.Lw;
-}
-// the first position that a row at p sees through its window
-SPEC_DEV int window_low(const PattnPlan& pl, int p) { return pl.window > 0 && p >= pl.window ? p - pl.window + 1 : 0; }
-
-// The rows of a block that share a chunk length (all of them, or the rows
-// before and after a step of chunk_len), and their chunk slots: the sinks'
-// chunks that end before the window, then the window's.
-struct Span {
-  int i0, i1;                // block rows [i0, i1)
-  int L, lo, last;           // tiles per chunk; first window key; last key
-  int sink_tiles, ns, cbase, nslots;
-};
-SPEC_DEV int span_count(const PattnPlan& pl, int n_past) {
-  return chunk_len(pl, n_past) == chunk_len(pl, n_past + pl.M - 1) ? 1 : 2;
-}
-SPEC_DEV Span span_of(const PattnPlan& pl, int n_past, int pass) {
-  Span s;
-  const int la = chunk_len(pl, n_past), lb = chunk_len(pl, n_past + pl.M - 1);
-  const int cut = la == lb ? pl.M : la * pl.C * kKeys - n_past;      // rows before the step
-  s.i0 = pass == 0 ? 0 : cut;
-  s.i1 = pass == 0 ? cut : pl.M;
-  s.L = pass == 0 ? la : lb;
-  s.lo = window_low(pl, n_past + s.i0);
-  s.last = n_past + s.i1 - 1;
-  s.sink_tiles = s.ns = s.cbase = s.nslots = 0;
-  if (s.last >= 0) {
-    const int keys = s.L * kKeys, sk = pl.window > 0 ? min(pl.sinks, s.last + 1) : 0;
-    s.sink_tiles = (sk + kKeys - 1) / kKeys;
-    s.cbase = s.lo / keys;
-    s.ns = min((s.sink_tiles + s.L - 1) / s.L, s.cbase);
-    s.nslots = s.ns + s.last / keys - s.cbase + 1;
-  }
-  return s;
-}
-// the key tiles of slot c: n0 from a0, then n - n0 from a1
-struct TileList {
-  int a0 = 0, n0 = 0, a1 = 0, n = 0;
-  SPEC_DEV int at(int j) const { return j < n0 ? a0 + j : a1 + (j - n0); }
-};
-SPEC_DEV TileList tiles_of(const Span& s, int c) {
-  TileList t;
-  if (c >= s.nslots) return t;
-  const int x = c < s.ns ? c : s.cbase + c - s.ns, from = x * s.L, to = from + s.L;
-  t.a0 = from;
-  t.n0 = max(0, min(to, s.sink_tiles) - from);
-  t.a1 = max(max(from, s.lo >> 7), from + t.n0);
-  t.n = t.n0 + max(0, min(to, (s.last >> 7) + 1) - t.a1);
-  return t;
-}
-
-SPEC_DEV uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
 
 using f2 = unsigned long long;                      // two floats for the packed fp32 instructions
 // binary16 parts of a pair: hi nearest, lo what is left (the first in the low half)
@@ -183,25 +118,6 @@ SPEC_DEV bool named_bar_or(int id, int count, bool pred) {
   return r != 0;
 }
 
-// loads issued where they stand (a plain load may be moved down to its use,
-// behind a wait)
-SPEC_DEV uint4 ldg_now(const uint4* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-SPEC_DEV uint32_t ldg_now(const void* p) {
-  uint32_t v;
-  asm volatile("ld.global.nc.u32 %0, [%1];\n" : "=r"(v) : "l"(p));
-  return v;
-}
-SPEC_DEV int page_at(const KvView& kv, int lp) {
-  const int page = lp < kv.max_seq_pages ? (int)ldg_now((const void*)(kv.page_table + lp)) : -1;
-  return page < kv.num_pages ? page : -1;
-}
-
 // One page of a tile as an unpacking warp holds it.
 // 4-bit: lane = key % 16 + 16 * d half; 64 codes and 4 scale bytes of K or V.
 struct Raw4 {
@@ -210,8 +126,8 @@ struct Raw4 {
 };
 // base: this lane's first chunk of page 0 of the layer and head; stride: bytes
 // of a page of the pool
-SPEC_DEV void load_page(const uint8_t* base, uint32_t stride, int page, int scales, Raw4& r) {
-  if (page < 0) {                                        // unmapped: zeros (its keys are masked)
+SPEC_DEV void load_page(const uint8_t* base, uint32_t stride, int page, bool there, int scales, Raw4& r) {
+  if (!there) {                                          // unmapped: zeros (its keys are masked)
     r.c[0] = r.c[1] = make_uint4(0, 0, 0, 0);
     r.s = 0;
     return;
@@ -244,8 +160,8 @@ SPEC_DEV void unpack_row(const uint4 (&codes)[2], uint32_t scales, uint8_t* row,
 struct Raw16 {
   uint4 x[8];
 };
-SPEC_DEV void load_rows(const uint4* base, uint32_t stride, int page, Raw16& r) {
-  if (page < 0) {
+SPEC_DEV void load_rows(const uint4* base, uint32_t stride, int page, bool there, Raw16& r) {
+  if (!there) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) r.x[j] = make_uint4(0, 0, 0, 0);
     return;
@@ -254,12 +170,12 @@ SPEC_DEV void load_rows(const uint4* base, uint32_t stride, int page, Raw16& r) 
 #pragma unroll
   for (int j = 0; j < 8; ++j) r.x[j] = ldg_now(p + 32 * j);
 }
-// bf16 pair as binary16; |x| >= 2^15, infinities and NaN are the caller's business
+// bf16 pair as binary16; |x| >= 2^16, infinities and NaN are the caller's business
 SPEC_DEV uint32_t bf16x2_to_f16x2(uint32_t w) {
   const __half2 h = __floats2half2_rn(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-constexpr uint32_t kBf16Limit = 0x4700u;            // bf16 bits of 2^15
+constexpr uint32_t kBf16Limit = 0x4780u;            // bf16 bits of 2^16: binary16 holds every bf16 value below
 
 // ---------------------------------------------------------------------------
 // partials: grid (slot, KV head, row tile)
@@ -316,6 +232,169 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  // ---------------------------------------------------------------- unpack
+  // Item g is page g % 8 of tile g / 8; warp id of `count` takes every count-th.
+  // A step waits, unpacks and signals for two pages at once, the V of one item
+  // and the K of the next (whose stage is freed earlier): a lone warp issues an
+  // instruction every four or five cycles, and two independent streams fill
+  // some of the gaps.  The registers hold the next step's pages.
+  auto unpack = [&](int id, int count) {
+    const int items = total * kPagesPerTile;
+    auto page_of = [&](int g) { return g < items ? page_at(kv, tile_at(g >> 3) * kPagesPerTile + (g & 7)) : -1; };
+    // this item's stage, once its former K (V) has been read
+    auto free_k = [&](int it) {
+      return it < kStages || __all_sync(0xffffffffu, mbar_wait(&k_free[it % kStages], ((it / kStages) - 1) & 1));
+    };
+    auto free_v = [&](int it) {
+      return it < kStages || __all_sync(0xffffffffu, mbar_wait(&v_free[it % kStages], ((it / kStages) - 1) & 1));
+    };
+    bool ok = true;
+    if constexpr (k4) {
+      const int t = lane & 15, half = lane >> 4;
+      uint8_t* row0 = sm + half * kHalf + t * 128;
+      const uint32_t stride = (uint32_t)(kv.n_layers * 2 * kv.n_kv) * kKv4PageBytes;
+      const uint8_t* kb = reinterpret_cast<const uint8_t*>(kv.pool) +
+                          (size_t)(layer * 2 * kv.n_kv + kvh) * kKv4PageBytes + kv4_chunk(t, 2 * half);
+      const uint8_t* vb = kb + kv.n_kv * kKv4PageBytes;
+      const int scales = kKv4Scales + 8 * t + 4 * half - kv4_chunk(t, 2 * half);
+      // the pages of this V, of this step's K, and of the K after that
+      int page = page_of(id), next = page_of(id + count), after = page_of(id + 2 * count);
+      Raw4 k, v;
+      load_page(kb, stride, page, page_ok(kv, page), scales, k);
+      load_page(vb, stride, page, page_ok(kv, page), scales, v);
+      for (int g = id - count; ok && g < items; g += count) {
+        const int gk = g + count, itk = gk >> 3, stk = itk % kStages, it = g >> 3, st = it % kStages;
+        const bool has_k = gk < items, has_v = g >= 0;
+        if (has_k) ok = free_k(itk);
+        if (has_v) ok = ok && free_v(it);
+        if (!ok) break;
+        if (has_k) unpack_row(k.c, k.s, row0 + stk * kStageBytes + (gk & 7) * 2048, t & 7);
+        if (has_v) unpack_row(v.c, v.s, row0 + st * kStageBytes + 2 * kHalf + (g & 7) * 2048, t & 7);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          if (has_k) {
+            mapped[itk & 7][gk & 7] = page_ok(kv, has_v ? next : page);
+            mbar_arrive(&k_full[stk]);
+          }
+          if (has_v) mbar_arrive(&v_full[st]);
+        }
+        // K of the step after; V of the item whose K was just unpacked
+        const int nk = has_v ? after : next;
+        load_page(kb, stride, nk, page_ok(kv, nk), scales, k);
+        if (has_v) {
+          load_page(vb, stride, next, page_ok(kv, next), scales, v);
+          page = next;
+          next = after;
+          after = page_of(gk + 2 * count);
+        }
+      }
+    } else {
+      // (16-byte units; a page of one head is 256 of them)
+      const uint32_t stride = (uint32_t)(kv.n_layers * 2 * kv.n_kv) * 256u;
+      const uint4* kb = reinterpret_cast<const uint4*>(kv.pool) + (size_t)(layer * 2 * kv.n_kv + kvh) * 256 + lane;
+      const uint4* vb = kb + kv.n_kv * 256;
+      int page = page_of(id), next = page_of(id + count), after = page_of(id + 2 * count);
+      Raw16 k, v;
+      load_rows(kb, stride, page, page_ok(kv, page), k);
+      load_rows(vb, stride, page, page_ok(kv, page), v);
+      // chunk j of this lane: row 2j + lane / 16, 16-byte chunk lane % 16
+      const int ch = lane & 15, rh = lane >> 4;
+      uint8_t* dst0 = sm + (ch >> 3) * kHalf + rh * 128;
+      auto put = [&](const Raw16& r, uint8_t* dst) {
+        __half2 top = __floats2half2_rn(0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint4 y = make_uint4(bf16x2_to_f16x2(r.x[j].x), bf16x2_to_f16x2(r.x[j].y), bf16x2_to_f16x2(r.x[j].z),
+                               bf16x2_to_f16x2(r.x[j].w));
+          const __half2* yh = reinterpret_cast<const __half2*>(&y);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = __hmax2_nan(top, __habs2(yh[e]));
+          *reinterpret_cast<uint4*>(dst + j * 256 + (((ch & 7) ^ ((2 * j + rh) & 7)) << 4)) = y;
+        }
+        const uint32_t m = *reinterpret_cast<const uint32_t*>(&top);
+        return (m & 0x7C00u) == 0x7C00u || (m & 0x7C000000u) == 0x7C000000u;     // past binary16, or not finite
+      };
+      // the same with every row looked at: elements past binary16 are zeroed
+      // and their rows returned; V rows that no row of the block sees are
+      // zeroed (stale bytes may be anything, and 0 * NaN is NaN).  Keys that no
+      // row sees are masked, so only the others count.
+      auto put_checked = [&](const Raw16& r, uint8_t* dst, bool is_v, int t0, bool there) {
+        uint32_t far = 0;
+#pragma unroll 1
+        for (int j = 0; j < 8; ++j) {
+          uint4 x = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e == j) x = r.x[e];
+          uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          const int t = t0 + 2 * j + rh;
+          const bool seen = there && t <= b_last && (t >= low0 || t < sinks);
+          bool big = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool lo = (w[e] & 0x7FFFu) >= kBf16Limit, hi = (w[e] >> 16 & 0x7FFFu) >= kBf16Limit;
+            big = big || lo || hi;
+            w[e] &= (lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0x0000FFFFu : 0xFFFFFFFFu);
+          }
+          const uint32_t m = __ballot_sync(0xffffffffu, big && seen);
+          far |= ((m & 0xFFFFu ? 1u : 0u) | (m >> 16 ? 2u : 0u)) << (2 * j);
+          uint4 y = make_uint4(bf16x2_to_f16x2(w[0]), bf16x2_to_f16x2(w[1]), bf16x2_to_f16x2(w[2]), bf16x2_to_f16x2(w[3]));
+          if (is_v && !seen) y = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(dst + j * 256 + (((ch & 7) ^ ((2 * j + rh) & 7)) << 4)) = y;
+        }
+        return far;
+      };
+      auto all_seen = [&](int t0, bool there) {
+        return there && t0 + 15 <= b_last && (t0 >= low0 || t0 + 16 <= sinks);
+      };
+      for (int g = id - count; ok && g < items; g += count) {
+        const int gk = g + count, itk = gk >> 3, stk = itk % kStages, it = g >> 3, st = it % kStages;
+        const bool has_k = gk < items, has_v = g >= 0;
+        if (has_k) ok = free_k(itk);
+        if (has_v) ok = ok && free_v(it);
+        if (!ok) break;
+        uint32_t fk = 0, fv = 0;
+        const int kpage = has_v ? next : page;
+        if (has_k) {
+          uint8_t* dst = dst0 + stk * kStageBytes + (gk & 7) * 2048;
+          const int t0 = tile_at(itk) * kKeys + 16 * (gk & 7);
+          if (__any_sync(0xffffffffu, put(k, dst))) fk = put_checked(k, dst, false, t0, page_ok(kv, kpage));
+        }
+        if (has_v) {
+          uint8_t* dst = dst0 + st * kStageBytes + 2 * kHalf + (g & 7) * 2048;
+          const int t0 = tile_at(it) * kKeys + 16 * (g & 7);
+          if (__any_sync(0xffffffffu, put(v, dst)) || !all_seen(t0, page_ok(kv, page)))
+            fv = put_checked(v, dst, true, t0, page_ok(kv, page));
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          if (has_k) {
+            mapped[itk & 7][gk & 7] = page_ok(kv, kpage);
+            odd[0][itk & 7][gk & 7] = (uint16_t)fk;
+            mbar_arrive(&k_full[stk]);
+          }
+          if (has_v) {
+            odd[1][it & 7][g & 7] = (uint16_t)fv;
+            mbar_arrive(&v_full[st]);
+          }
+        }
+        const int nk = has_v ? after : next;
+        load_rows(kb, stride, nk, page_ok(kv, nk), k);
+        if (has_v) {
+          load_rows(vb, stride, next, page_ok(kv, next), v);
+          page = next;
+          next = after;
+          after = page_of(gk + 2 * count);
+        }
+      }
+    }
+    if (!ok && lane == 0) atomicOr(status, SPEC_ST_DEVICE_WAIT);
+  };
+  // softmax warps without rows unpack as well
+  const int unpackers = kUnpackWarps + 2 * (4 - row_warps);
+
   // (total == 0: nothing of this chunk is seen)
   if (warp >= kSoftWarps) {
   if constexpr (k4)
@@ -324,144 +403,7 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n");
   if (total == 0) {
   } else if (warp >= kWLoad) {
-    // -------------------------------------------------------------- unpack
-    // item g is page g % 8 of tile g / 8; this warp takes every sixth
-    const int items = total * kPagesPerTile, g0 = warp - kWLoad;
-    auto page_of = [&](int g) { return g < items ? page_at(kv, tile_at(g >> 3) * kPagesPerTile + (g & 7)) : -1; };
-    auto free_k = [&](int it) {
-      return it < kStages || __all_sync(0xffffffffu, mbar_wait(&k_free[it % kStages], ((it / kStages) - 1) & 1));
-    };
-    auto free_v = [&](int it) {
-      return it < kStages || __all_sync(0xffffffffu, mbar_wait(&v_free[it % kStages], ((it / kStages) - 1) & 1));
-    };
-    auto done = [&](uint64_t* bar) {
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar);
-    };
-    bool ok = true;
-    if constexpr (k4) {
-      // K runs one item ahead of V, whose stage is freed later; the registers
-      // hold the next item of each besides
-      const int t = lane & 15, half = lane >> 4;
-      auto row_of = [&](int g) {
-        return sm + (size_t)((g >> 3) % kStages) * kStageBytes + half * kHalf + (16 * (g & 7) + t) * 128;
-      };
-      auto put_k = [&](int g, const Raw4& r, int page) {
-        if (!free_k(g >> 3)) return false;
-        unpack_row(r.c, r.s, row_of(g), t & 7);
-        if (lane == 0) mapped[(g >> 3) & 7][g & 7] = page >= 0;
-        done(&k_full[(g >> 3) % kStages]);
-        return true;
-      };
-      auto put_v = [&](int g, const Raw4& r) {
-        if (!free_v(g >> 3)) return false;
-        unpack_row(r.c, r.s, row_of(g) + 2 * kHalf, t & 7);
-        done(&v_full[(g >> 3) % kStages]);
-        return true;
-      };
-      const uint32_t stride = (uint32_t)(kv.n_layers * 2 * kv.n_kv) * kKv4PageBytes;
-      const uint8_t* kb0 = reinterpret_cast<const uint8_t*>(kv.pool) +
-                           (size_t)(layer * 2 * kv.n_kv + kvh) * kKv4PageBytes + kv4_chunk(t, 2 * half);
-      const uint8_t* vb0 = kb0 + kv.n_kv * kKv4PageBytes;
-      const int scales = kKv4Scales + 8 * t + 4 * half - kv4_chunk(t, 2 * half);
-      Raw4 ka, kb, va, vb;
-      const int p0 = page_of(g0), p1 = page_of(g0 + kUnpackWarps);
-      // the pages whose K is next, loaded next and loaded after that: a page
-      // id is fetched a step before its page
-      int held = p1, next = page_of(g0 + 2 * kUnpackWarps), after = page_of(g0 + 3 * kUnpackWarps);
-      load_page(kb0, stride, p0, scales, ka);
-      load_page(kb0, stride, p1, scales, kb);
-      load_page(vb0, stride, p0, scales, va);
-      load_page(vb0, stride, p1, scales, vb);
-      if (g0 < items) ok = put_k(g0, ka, p0);
-      // one item: V of g, K of the item after it (whose K is in kn), loads of
-      // the item after that into the registers that become free
-      auto step = [&](int g, Raw4& vg, Raw4& kg, const Raw4& kn) {
-        const int id = page_of(g + 4 * kUnpackWarps);
-        load_page(kb0, stride, next, scales, kg);       // kg's page has been unpacked
-        if (g + kUnpackWarps < items && !put_k(g + kUnpackWarps, kn, held)) return false;
-        if (!put_v(g, vg)) return false;
-        load_page(vb0, stride, next, scales, vg);
-        held = next;
-        next = after;
-        after = id;
-        return true;
-      };
-      for (int g = g0; ok && g < items; g += 2 * kUnpackWarps) {
-        ok = step(g, va, ka, kb);
-        if (ok && g + kUnpackWarps < items) ok = step(g + kUnpackWarps, vb, kb, ka);
-      }
-    } else {
-      // registers hold the next item of K and of V
-      Raw16 k, v;
-      // (16-byte units; a page of one head is 256 of them)
-      const uint32_t stride = (uint32_t)(kv.n_layers * 2 * kv.n_kv) * 256u;
-      const uint4* kb0 = reinterpret_cast<const uint4*>(kv.pool) + (size_t)(layer * 2 * kv.n_kv + kvh) * 256 + lane;
-      const uint4* vb0 = kb0 + kv.n_kv * 256;
-      // the pages in v, in k, and of the K after that
-      int page = page_of(g0), next = page_of(g0 + kUnpackWarps), after = page_of(g0 + 2 * kUnpackWarps);
-      load_rows(kb0, stride, page, k);
-      load_rows(vb0, stride, page, v);
-      auto put = [&](Raw16& r, int st, int u, int which, int t0, bool there) -> uint32_t {
-        uint32_t far = 0;                               // rows (of the 16) with an element out of range
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int row = 2 * j + (lane >> 4), key = 16 * u + row, t = t0 + 16 * u + row, ch = lane & 15;
-          uint32_t w[4] = {r.x[j].x, r.x[j].y, r.x[j].z, r.x[j].w};
-          uint32_t top = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = __vmaxu2(top, w[e] & 0x7FFF7FFFu);
-          // a key that some row sees; others are masked, and their V is zeroed
-          // (stale bytes may be anything, and 0 * NaN is NaN)
-          const bool seen = there && t <= b_last && (t >= low0 || t < sinks);
-          const bool big = seen && ((top & 0xFFFFu) >= kBf16Limit || (top >> 16) >= kBf16Limit);
-          const uint32_t m = __ballot_sync(0xffffffffu, big);
-          far |= ((m & 0xFFFFu ? 1u : 0u) | (m >> 16 ? 2u : 0u)) << (2 * j);
-          if (big) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] &= ((w[e] & 0x7FFFu) >= kBf16Limit ? 0xFFFF0000u : 0xFFFFFFFFu) &
-                      ((w[e] >> 16 & 0x7FFFu) >= kBf16Limit ? 0xFFFFu : 0xFFFFFFFFu);
-          }
-          uint4 y = make_uint4(bf16x2_to_f16x2(w[0]), bf16x2_to_f16x2(w[1]), bf16x2_to_f16x2(w[2]), bf16x2_to_f16x2(w[3]));
-          if (which == 1 && !seen) y = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(sm + (size_t)st * kStageBytes + (2 * which + (ch >> 3)) * kHalf + key * 128 +
-                                    (((ch & 7) ^ (key & 7)) << 4)) = y;
-        }
-        return far;
-      };
-      // K runs one item ahead of V, whose stage is freed later
-      auto put_k = [&](int g, int pg) {
-        const uint32_t far = put(k, (g >> 3) % kStages, g & 7, 0, tile_at(g >> 3) * kKeys, pg >= 0);
-        if (lane == 0) {
-          mapped[(g >> 3) & 7][g & 7] = pg >= 0;
-          odd[0][(g >> 3) & 7][g & 7] = (uint16_t)far;
-        }
-        done(&k_full[(g >> 3) % kStages]);
-      };
-      if (g0 < items) put_k(g0, page);
-      load_rows(kb0, stride, next, k);
-      for (int g = g0; g < items; g += kUnpackWarps) {
-        const int it = g >> 3, st = it % kStages, gn = g + kUnpackWarps, id = page_of(gn + 2 * kUnpackWarps);
-        if (gn < items) {
-          ok = free_k(gn >> 3);
-          if (!ok) break;
-          put_k(gn, next);
-          load_rows(kb0, stride, after, k);
-        }
-        ok = free_v(it);
-        if (!ok) break;
-        const uint32_t far = put(v, st, g & 7, 1, tile_at(it) * kKeys, page >= 0);
-        if (lane == 0) odd[1][it & 7][g & 7] = (uint16_t)far;
-        done(&v_full[st]);
-        load_rows(vb0, stride, next, v);
-        page = next;
-        next = after;
-        after = id;
-      }
-    }
-    if (!ok && lane == 0) atomicOr(status, SPEC_ST_DEVICE_WAIT);
+    unpack(warp - kWLoad, unpackers);
   } else if (warp == kWQk) {
     // ------------------------------------------------------------ S = Q . K^T
     // D f32 (bit 4), A and B f16, N >> 3 at 17, M >> 4 at 24; 8 d steps of 16,
@@ -531,12 +473,15 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
     asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n");
   else
     asm volatile("setmaxnreg.inc.sync.aligned.u32 160;\n");
-  if (total > 0 && (warp & 3) < row_warps) {
+  if (total == 0) {
+  } else if ((warp & 3) >= row_warps) {
+    unpack(kUnpackWarps + (warp >> 2) * (4 - row_warps) + (warp & 3) - row_warps, unpackers);
+  } else {
     // ------------------------------------------------------------ softmax
     const int h = warp >> 2, ww = warp & 3;
     const int r = 32 * ww + lane, fr = r0 + r;          // tile row, row of the KV head
     const bool live = r < nr;
-    const int i = live ? fr / pl.group : 0, hd = live ? fr - i * pl.group : 0;
+    const int i = live ? div24(fr, pl.group) : 0, hd = live ? fr - i * pl.group : 0;
     const uint32_t tl = tmem + ((uint32_t)(32 * ww) << 16);
     constexpr float kBias = 7.f;                        // p = 2^(7 + s - max): binary16 keeps 2^-24 of 2^7
     const float* qr = q + ((size_t)i * pl.nq + kvh * pl.group + hd) * 128;
@@ -802,22 +747,21 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 pattn_merge_kernel(const float* __restrict__ part_o, const float2* __restrict__ part_ml, PattnPlan pl,
                    const int32_t* __restrict__ seq_len, float* __restrict__ out) {
   pdl_trigger();
-  pdl_wait();
   const int item = blockIdx.x * kMergeWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int i = div24(item, pl.nq), head = item - i * pl.nq, kvh = div24(head, pl.group);
+  pdl_wait();
   if (item >= pl.M * pl.nq) return;
-  const int i = item / pl.nq, head = item % pl.nq, kvh = head / pl.group;
   const int n_past = __ldcg(seq_len) - pl.M;
   Span s = span_of(pl, n_past, 0);
   if (i >= s.i1) s = span_of(pl, n_past, 1);
   const int n = n_past + i < 0 ? 0 : min(s.nslots, pl.slots);
   const size_t stride = (size_t)pl.nkv * pl.M * pl.group;
-  const size_t at = (size_t)kvh * pl.M * pl.group + i * pl.group + head % pl.group;
+  const size_t at = (size_t)kvh * pl.M * pl.group + i * pl.group + (head - kvh * pl.group);
   float m = -INFINITY;
   for (int c = lane; c < n; c += 32) {
-    const float2 x = part_ml[at + c * stride];
+    const float2 x = __ldcg(part_ml + at + c * stride);
     if (x.y != 0.f) m = fmaxf(m, x.x);
   }
-  m = warp_max(m);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float L = 0.f;
   constexpr int kBatch = 16;                            // loads in flight
@@ -825,8 +769,9 @@ pattn_merge_kernel(const float* __restrict__ part_o, const float2* __restrict__ 
     float4 y[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k)
-      if (c0 + k < n) y[k] = reinterpret_cast<const float4*>(part_o + (at + (c0 + k) * stride) * 128)[lane];
-    const float2 x = lane < kBatch && c0 + lane < n ? part_ml[at + (c0 + lane) * stride] : make_float2(0.f, 0.f);
+      if (c0 + k < n) y[k] = __ldcg(reinterpret_cast<const float4*>(part_o + (at + (c0 + k) * stride) * 128) + lane);
+    const float2 x = lane < kBatch && c0 + lane < n ? __ldcg(part_ml + at + (c0 + lane) * stride) : make_float2(0.f, 0.f);
+    if (c0 == 0) m = warp_max(m);
     const float wl = x.y != 0.f ? exp2f(x.x - m) : 0.f;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
@@ -845,12 +790,18 @@ pattn_merge_kernel(const float* __restrict__ part_o, const float2* __restrict__ 
       none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x / L, o.y / L, o.z / L, o.w / L);
 }
 
-// chunks of a KV head at most: one per SM and KV head.  At least 4, so that a
-// window's chunks (one of sinks, and one more than the window's own) fit.
-static int pattn_chunks(int nkv, int num_sms) { return num_sms / nkv > 4 ? num_sms / nkv : 4; }
+// chunks of a KV head at most: one per SM, KV head and row tile, so that the
+// grid is one wave.  (With as many for two row tiles, two waves, 16 rows of 13
+// heads take 57 instead of 45 us behind 32k keys.)  At least 4, so that
+// a window's chunks (one of sinks, and one more than the window's own) fit.
+static int pattn_chunks(int nkv, int row_tiles, int num_sms) {
+  const int c = num_sms / (nkv * row_tiles);
+  return c > 4 ? c : 4;
+}
 
 size_t paged_attention_floats(int nq, int nkv, int max_rows, int num_sms) {
-  return (size_t)pattn_chunks(nkv, num_sms) * nq * max_rows * 130;
+  // rows * chunks is largest for one row tile or, below 4 chunks, for all rows
+  return (size_t)pattn_chunks(nkv, 1, num_sms) * nq * max_rows * 130;
 }
 
 template <bool k4>
@@ -882,7 +833,9 @@ cudaError_t launch_paged_attention(bool k4, const KvView& kv, int layer, const f
   pl.group = nq / kv.n_kv;
   pl.window = window;
   pl.sinks = sinks;
-  pl.C = pattn_chunks(kv.n_kv, num_sms);
+  const int R = M * pl.group, row_tiles = (R + 127) / 128;
+  pl.C = pattn_chunks(kv.n_kv, row_tiles, num_sms);
+  pl.c_inv = ((1ull << 40) + pl.C - 1) / pl.C;
   // chunk slots: never more than the cache has tiles; the window's longest
   // chunk is the shortest with which sinks and window fit into C chunks
   const long long tiles = ((long long)kv.max_seq_pages * 16 + kKeys - 1) / kKeys;
@@ -896,12 +849,12 @@ cudaError_t launch_paged_attention(bool k4, const KvView& kv, int layer, const f
     pl.Lw = (int)(L < INT32_MAX ? L : INT32_MAX);
     if (pl.Lw == 1 && ss + ws < pl.slots) pl.slots = (int)(ss + ws);
   }
-  const int R = M * pl.group, row_tiles = (R + 127) / 128;
   pl.tile_rows = (R + row_tiles - 1) / row_tiles;
   float2* ml = reinterpret_cast<float2*>(part);        // [slots][nkv][R], then the outputs
   float* po = part + 2 * (size_t)pl.C * nq * 16;
-  cudaError_t e = k4 ? launch_pattn<true>(pl, kv, layer, q, row_tiles, po, ml, status, st)
-                     : launch_pattn<false>(pl, kv, layer, q, row_tiles, po, ml, status, st);
+  cudaError_t e = R <= kFewRows ? launch_pattn_few(k4, pl, kv, layer, q, po, ml, st)
+                  : k4          ? launch_pattn<true>(pl, kv, layer, q, row_tiles, po, ml, status, st)
+                                : launch_pattn<false>(pl, kv, layer, q, row_tiles, po, ml, status, st);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -1,0 +1,519 @@
+// pattn_few.cu — the partials of attention over a paged cache (pattn.cu) for calls
+// of at most 16 query rows per KV head: one decoded token of a group of up to 16
+// heads, a few rows of smaller groups.
+//
+// What bounds it.  A key tile is 18 KB (4-bit) or 64 KB (bf16), 800 or 2,850 cycles
+// of an SM's share of HBM.  The tcgen05 kernel pays for 128 rows whatever their
+// number, and for unpacking the tile into shared memory; it is bound by
+// instruction issue, at 4,000 cycles a tile.  Here the 16 rows are one m16n8k16
+// fragment, and the pages go from global memory into registers in the order of
+// the MMA's B fragment, with no shared memory and no barrier on the way: 512
+// (bf16: 768) warp MMAs a tile, 2.02 cycles each per SM.
+//
+// The warps of a CTA (slot, KV head) take the pages of its chunk in turn, with
+// a running (max, sum) and O of their own in registers; they are joined in order
+// at the end.  A page falls to the warp of its number mod 8, so a row's bits do
+// not depend on the block.
+//
+// The d's of a K row and the d's and keys of a V page may be visited in any
+// order.  Lane 4n + g (g < 4) takes d's 32 g .. of K (one 16-byte chunk of codes, 64
+// bytes of bf16), and d's 16 n .. of keys 4 g .. of V:
+//   S: B fragment of MMA ks: elements 4 ks .. 4 ks + 3 of the lane's chunk; column n
+//      of key tile nt (of two) is key 4 (n / 2) + n % 2 + 2 nt, so that a lane's
+//      scores are those of keys 4 g .. 4 g + 3, its V rows
+//   O: column n of MMA j is d 16 n + j
+//
+// Precision: as pattn.cu for the 4-bit cache (binary16, q and p in two parts,
+// row-wise powers of two).  bf16 pages are operands as they are, with q and p in
+// three bf16 parts (24 significant bits): no value is out of range.
+#include "common.cuh"
+#include "internal.h"
+#include "kv4.cuh"
+#include "pattn_plan.cuh"
+
+namespace spec {
+
+constexpr int kFewWarps = 8;
+constexpr int kOPitch = 132;               // floats between rows of a warp's O in shared memory
+constexpr size_t kFewSmem = sizeof(float) * kFewWarps * kFewRows * kOPitch;
+
+template <bool k4>
+SPEC_DEV void mma16816(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  if constexpr (k4)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+SPEC_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+// the operand part of a pair (x0 in the low half); x becomes what is left
+template <bool k4>
+SPEC_DEV uint32_t take_part(float& x0, float& x1) {
+  if constexpr (k4) {
+    const __half2 h = __floats2half2_rn(x0, x1);
+    const float2 f = __half22float2(h);
+    x0 -= f.x;
+    x1 -= f.y;
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
+    x0 -= __uint_as_float(u << 16);
+    x1 -= __uint_as_float(u & 0xFFFF0000u);
+    return u;
+  }
+}
+
+// A page as a lane loads it: K chunks of its key of both key tiles, V pieces of
+// its four keys
+template <bool k4>
+struct FewPage;
+template <>
+struct FewPage<true> {
+  uint4 k[2];
+  uint2 v[4];
+  uint32_t ks, vs;                         // word `lane` of the scales: groups 4 (lane % 2).. of key lane / 2
+};
+template <>
+struct FewPage<false> {
+  uint4 k[2][4], v[4][2];
+};
+SPEC_DEV uint2 ldg64_now(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+SPEC_DEV uint4 ldg128_now(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+// p: the K (V) page of the head
+SPEC_DEV void few_load_k(const uint8_t* p, int lane, FewPage<true>& r) {
+  const int n = lane >> 2, g = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt) r.k[nt] = ldg128_now(p + kv4_chunk(4 * (n >> 1) + (n & 1) + 2 * nt, g));
+  r.ks = ldg_now((const void*)(p + kKv4Scales + 4 * lane));
+}
+SPEC_DEV void few_load_v(const uint8_t* p, int lane, FewPage<true>& r) {
+  const int n = lane >> 2, g = lane & 3;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) r.v[e] = ldg64_now(p + kv4_chunk(4 * g + e, n >> 1) + 8 * (n & 1));
+  r.vs = ldg_now((const void*)(p + kKv4Scales + 4 * lane));
+}
+SPEC_DEV void few_load_k(const uint8_t* p, int lane, FewPage<false>& r) {
+  const int n = lane >> 2, g = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) r.k[nt][c] = ldg128_now(p + 256 * (4 * (n >> 1) + (n & 1) + 2 * nt) + 64 * g + 16 * c);
+}
+SPEC_DEV void few_load_v(const uint8_t* p, int lane, FewPage<false>& r) {
+  const int n = lane >> 2, g = lane & 3;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) r.v[e][c] = ldg128_now(p + 256 * (4 * g + e) + 32 * n + 16 * c);
+}
+SPEC_DEV uint32_t word_of(const uint4& x, int i) { return i == 0 ? x.x : (i == 1 ? x.y : (i == 2 ? x.z : x.w)); }
+// f16 pair of byte b of w
+template <int B>
+SPEC_DEV uint32_t e2m1_byte(uint32_t w) {
+  uint32_t r;
+  if constexpr (B == 0) asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %1;\n cvt.rn.f16x2.e2m1x2 %0, a;\n}\n" : "=r"(r) : "r"(w));
+  if constexpr (B == 1) asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %1;\n cvt.rn.f16x2.e2m1x2 %0, b;\n}\n" : "=r"(r) : "r"(w));
+  if constexpr (B == 2) asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %1;\n cvt.rn.f16x2.e2m1x2 %0, c;\n}\n" : "=r"(r) : "r"(w));
+  if constexpr (B == 3) asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %1;\n cvt.rn.f16x2.e2m1x2 %0, d;\n}\n" : "=r"(r) : "r"(w));
+  return r;
+}
+SPEC_DEV uint32_t e2m1_pick(uint32_t w, int b) {        // b known at compile time after unrolling
+  return b == 0 ? e2m1_byte<0>(w) : (b == 1 ? e2m1_byte<1>(w) : (b == 2 ? e2m1_byte<2>(w) : e2m1_byte<3>(w)));
+}
+SPEC_DEV uint32_t scale_pair(uint32_t byte) { return min(byte, (uint32_t)kKv4TopScale) * 0x00800080u; }
+
+template <bool k4>
+__global__ void __launch_bounds__(32 * kFewWarps, 1)
+pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, float* __restrict__ part_o,
+                 float2* __restrict__ part_ml) {
+  constexpr int kParts = k4 ? 2 : 3;                    // of q and p
+  constexpr float kBias = k4 ? 7.f : 0.f;               // p = 2^(bias + s - max)
+  constexpr int kPageBytes = k4 ? kKv4PageBytes : 4096;
+  extern __shared__ __align__(16) float o_sm[];         // [warp][row][kOPitch]
+  __shared__ uint4 qs[kParts][8][32];                   // A fragments
+  __shared__ int qmax[kFewRows];
+  __shared__ float2 ml_sm[kFewWarps][kFewRows];
+  __shared__ uint32_t poison;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = lane >> 2, g = lane & 3;
+  const int slot = blockIdx.x, kvh = blockIdx.y, R = pl.M * pl.group;
+  if (tid < kFewRows) qmax[tid] = 0;
+  if (tid == 32) poison = 0;
+  pdl_trigger();
+  pdl_wait();
+  const int n_past = __ldcg(kv.seq_len) - pl.M;
+  // this thread's rows n and n + 8; in the first 8 warps Q elements 32 g + 4 warp
+  // .. (MMA `warp`'s)
+  float4 qv[2];
+  int pos[2], plow[2], row_i[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = n + 8 * h;
+    row_i[h] = r < R ? r / pl.group : -1;
+    pos[h] = n_past + row_i[h];
+    plow[h] = window_low(pl, pos[h]);
+    qv[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < R && warp < 8)
+      qv[h] = *reinterpret_cast<const float4*>(
+          q + ((size_t)row_i[h] * pl.nq + kvh * pl.group + r - row_i[h] * pl.group) * 128 + 32 * g + 4 * warp);
+  }
+  const int passes = span_count(pl, n_past);
+  TileList tl0 = tiles_of(span_of(pl, n_past, 0), slot), tl1;
+  if (passes == 2) tl1 = tiles_of(span_of(pl, n_past, 1), slot);
+  if (tl0.n + tl1.n == 0) return;
+  const int b_last = n_past + pl.M - 1;                 // the block's last position
+  const int low0 = window_low(pl, n_past), low1 = window_low(pl, b_last), sinks = pl.window > 0 ? pl.sinks : 0;
+
+  // log2(e) / sqrt(d), for the 4-bit cache times the row's power of two
+  float unit[2];
+  unit[0] = unit[1] = 1.4426950408889634f / sqrtf(128.0f);
+  __syncthreads();
+  if (k4) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float m = fmaxf(fmaxf(fabsf(qv[h].x), fabsf(qv[h].y)), fmaxf(fabsf(qv[h].z), fabsf(qv[h].w)));
+      atomicMax(&qmax[n + 8 * h], __float_as_int(m));   // magnitudes order as integers
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int e = min(max(((qmax[n + 8 * h] >> 23) & 255) - 127, -100), 100);
+      const float mul = __uint_as_float((uint32_t)(127 - e) << 23);
+      unit[h] *= __uint_as_float((uint32_t)(127 + e) << 23);
+      qv[h].x *= mul;
+      qv[h].y *= mul;
+      qv[h].z *= mul;
+      qv[h].w *= mul;
+    }
+  }
+#pragma unroll
+  for (int pt = 0; pt < kParts; ++pt) {
+    uint4 a;
+    a.x = take_part<k4>(qv[0].x, qv[0].y);
+    a.y = take_part<k4>(qv[1].x, qv[1].y);
+    a.z = take_part<k4>(qv[0].z, qv[0].w);
+    a.w = take_part<k4>(qv[1].z, qv[1].w);
+    if (warp < 8) qs[pt][warp][lane] = a;
+  }
+  __syncthreads();
+
+  const uint32_t stride = (uint32_t)(kv.n_layers * 2 * kv.n_kv * kPageBytes);
+  const uint8_t* kbase = reinterpret_cast<const uint8_t*>(kv.pool) + (size_t)(layer * 2 * kv.n_kv + kvh) * kPageBytes;
+  const uint8_t* vbase = kbase + (size_t)kv.n_kv * kPageBytes;
+
+#pragma unroll 1
+  for (int pass = 0; pass < passes; ++pass) {
+    const Span sp = span_of(pl, n_past, pass);
+    const TileList tl = pass == 0 ? tl0 : tl1;
+    bool mine[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) mine[h] = row_i[h] >= sp.i0 && row_i[h] < sp.i1;
+    float o[16][4];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    float ref[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
+
+    // This warp's pages: those of the chunk whose number is `warp` mod 12.  K of
+    // the next one is loaded once K of this one has been used, V likewise; page
+    // ids are fetched a step earlier.
+    const int n0 = tl.n0 * kPagesPerTile, n1 = (tl.n - tl.n0) * kPagesPerTile;
+    auto first_of = [&](int from) { return (int)((unsigned)(warp + kFewWarps - (unsigned)from % kFewWarps) % kFewWarps); };
+    const int f0 = first_of(tl.a0 * kPagesPerTile), f1 = first_of(tl.a1 * kPagesPerTile);
+    const int c0 = n0 > f0 ? (n0 - f0 + kFewWarps - 1) / kFewWarps : 0;
+    const int pages = c0 + (n1 > f1 ? (n1 - f1 + kFewWarps - 1) / kFewWarps : 0);
+    auto page_no = [&](int j) {
+      return j < c0 ? tl.a0 * kPagesPerTile + f0 + kFewWarps * j : tl.a1 * kPagesPerTile + f1 + kFewWarps * (j - c0);
+    };
+    auto id_of = [&](int j) { return j < pages ? page_at(kv, page_no(j)) : -1; };
+    // a mapped page with a key that some row of the block sees
+    auto wanted = [&](int j, int page) {
+      if (j >= pages || !page_ok(kv, page)) return false;
+      const int k0 = 16 * page_no(j);
+      return k0 <= b_last && (k0 + 15 >= low0 || k0 < sinks);
+    };
+    FewPage<k4> cur;
+    int id0 = id_of(0), id1 = id_of(1);
+    bool want = wanted(0, id0);
+    if (want) {
+      few_load_k(kbase + (uint64_t)(uint32_t)id0 * stride, lane, cur);
+      few_load_v(vbase + (uint64_t)(uint32_t)id0 * stride, lane, cur);
+    }
+#pragma unroll 1
+    for (int j = 0; j < pages; ++j) {
+      const int id2 = id_of(j + 2);
+      const bool want1 = wanted(j + 1, id1);
+      const uint8_t* knext = kbase + (uint64_t)(uint32_t)id1 * stride;
+      const uint8_t* vnext = vbase + (uint64_t)(uint32_t)id1 * stride;
+      if (want) {
+        const int k0 = 16 * page_no(j);
+        // ------------------------------------------------ S = Q . K^T
+        float s[2][2][4] = {};                          // [key tile][high part, low parts]
+        uint32_t ksc[2][2];
+        if constexpr (k4) {
+          // scales 2 g and 2 g + 1 of this lane's keys
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            const uint32_t w =
+                __shfl_sync(0xffffffffu, cur.ks, 2 * (4 * (n >> 1) + (n & 1) + 2 * nt) + (g >> 1)) >> (16 * (g & 1));
+            ksc[nt][0] = scale_pair(w & 0xFFu);
+            ksc[nt][1] = scale_pair((w >> 8) & 0xFFu);
+          }
+        }
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          uint32_t b[2][2];
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            if constexpr (k4) {
+              const uint32_t w = word_of(cur.k[nt], ks >> 1), s2 = ksc[nt][ks >> 2];
+              b[nt][0] = hmul2_u32(e2m1_pick(w, 2 * (ks & 1)), s2);
+              b[nt][1] = hmul2_u32(e2m1_pick(w, 2 * (ks & 1) + 1), s2);
+            } else {
+              b[nt][0] = word_of(cur.k[nt][ks >> 1], 2 * (ks & 1));
+              b[nt][1] = word_of(cur.k[nt][ks >> 1], 2 * (ks & 1) + 1);
+            }
+          }
+#pragma unroll
+          for (int pt = kParts - 1; pt >= 0; --pt) {
+            const uint4 a = qs[pt][ks][lane];
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) mma16816<k4>(s[nt][pt > 0], a, b[nt][0], b[nt][1]);
+          }
+        }
+        if (want1) few_load_k(knext, lane, cur);
+        // x[h][e]: row n + 8 h, key k0 + 4 g + e
+        float x[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[h][e] = (s[e >> 1][0][2 * h + (e & 1)] + s[e >> 1][1][2 * h + (e & 1)]) * unit[h];
+        // some row of the block does not see some key of the page
+        const bool masked = k0 + 15 > n_past || (k0 < low1 && k0 + 16 > sinks) || passes > 1;
+        if (masked) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int t = k0 + 4 * g + e;
+              if (!(mine[h] && t <= pos[h] && (t >= plow[h] || t < sinks))) x[h][e] = -INFINITY;
+            }
+          if constexpr (!k4) {
+            // V rows that no row sees are zeroed (stale bytes may be anything,
+            // and 0 * NaN is NaN); a non-finite element that only some rows see
+            // is taken out, and those rows get it at the end
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int t = k0 + 4 * g + e;
+              const bool seen = t <= b_last && (t >= low0 || t < sinks);
+              const bool by_all = t <= n_past && (t >= low1 || t < sinks);
+              bool bad = false;
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                uint32_t* w = reinterpret_cast<uint32_t*>(&cur.v[e][c]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const bool lo = (w[i] & 0x7F80u) == 0x7F80u, hi = (w[i] & 0x7F800000u) == 0x7F800000u;
+                  if (!seen) {
+                    w[i] = 0;
+                  } else if (!by_all && (lo || hi)) {
+                    bad = true;
+                    w[i] &= (lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0x0000FFFFu : 0xFFFFFFFFu);
+                  }
+                }
+              }
+              // bit b: key n_past + 1 + b (b < 16) or low0 + b - 16
+              if (bad) atomicOr(&poison, 1u << (t > n_past ? t - n_past - 1 : 16 + t - low0));
+            }
+          }
+        }
+        float mx[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) mx[h] = fmaxf(fmaxf(x[h][0], x[h][1]), fmaxf(x[h][2], x[h][3]));
+        // the reference moves only when a score exceeds it by more than 8
+        if (__any_sync(0xffffffffu, mx[0] > ref[0] + 8.f || mx[1] > ref[1] + 8.f)) {
+          float a[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+            a[h] = 1.f;
+            if (mx[h] > ref[h] + 8.f) {
+              if (ref[h] != -INFINITY) a[h] = ex2(ref[h] - mx[h]);
+              ref[h] = mx[h];
+            }
+            lsum[h] *= a[h];
+          }
+#pragma unroll
+          for (int jj = 0; jj < 16; ++jj) {
+            o[jj][0] *= a[0];
+            o[jj][1] *= a[0];
+            o[jj][2] *= a[1];
+            o[jj][3] *= a[1];
+          }
+        }
+        uint4 pa[kParts];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float base = kBias - (ref[h] == -INFINITY ? 0.f : ref[h]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[h][e] = ex2(x[h][e] + base);
+            lsum[h] += x[h][e];
+          }
+        }
+#pragma unroll
+        for (int pt = 0; pt < kParts; ++pt) {
+          pa[pt].x = take_part<k4>(x[0][0], x[0][1]);
+          pa[pt].y = take_part<k4>(x[1][0], x[1][1]);
+          pa[pt].z = take_part<k4>(x[0][2], x[0][3]);
+          pa[pt].w = take_part<k4>(x[1][2], x[1][3]);
+        }
+        // ------------------------------------------------ O += P . V
+        uint32_t s2[4];
+        if constexpr (k4) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)                   // scale byte n of keys 4 g + e
+            s2[e] = scale_pair((__shfl_sync(0xffffffffu, cur.vs, 2 * (4 * g + e) + (n >> 2)) >> (8 * (n & 3))) & 0xFFu);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {                // d's 16 n + 2i .. 2i + 3: four independent sums
+          uint32_t b[4][2];
+#pragma unroll
+          for (int ii = 0; ii < 2; ++ii) {
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (k4)
+                v[e] = hmul2_u32(e2m1_pick(i < 4 ? cur.v[e].x : cur.v[e].y, (i & 3) + ii), s2[e]);
+              else
+                v[e] = word_of(cur.v[e][i >> 2], (i & 3) + ii);
+            }
+#pragma unroll
+            for (int hl = 0; hl < 2; ++hl) {
+              const uint32_t sel = hl ? 0x7632u : 0x5410u;
+              b[2 * ii + hl][0] = __byte_perm(v[0], v[1], sel);
+              b[2 * ii + hl][1] = __byte_perm(v[2], v[3], sel);
+            }
+          }
+#pragma unroll
+          for (int pt = kParts - 1; pt >= 0; --pt)
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) mma16816<k4>(o[2 * i + jj], pa[pt], b[jj][0], b[jj][1]);
+        }
+      }
+      if (want1) {
+        if (!want) few_load_k(knext, lane, cur);
+        few_load_v(vnext, lane, cur);
+      }
+      want = want1;
+      id0 = id1;
+      id1 = id2;
+    }
+    // ---- join the warps, in order.  Row n + 8 h, d's 32 g + 16 e + (MMA index).
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      lsum[h] += __shfl_xor_sync(0xffffffffu, lsum[h], 1);
+      lsum[h] += __shfl_xor_sync(0xffffffffu, lsum[h], 2);
+      if (g == 0) ml_sm[warp][n + 8 * h] = make_float2(ref[h] - kBias, lsum[h]);
+      float* dst = o_sm + ((size_t)warp * kFewRows + n + 8 * h) * kOPitch + 32 * g;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          // the lanes of a store phase are two rows and four g: pieces in an
+          // order rotated by g fall into different banks
+          const int cc = (c + g) & 3;
+          float4 y;
+          y.x = cc == 0 ? o[0][2 * h + e] : (cc == 1 ? o[4][2 * h + e] : (cc == 2 ? o[8][2 * h + e] : o[12][2 * h + e]));
+          y.y = cc == 0 ? o[1][2 * h + e] : (cc == 1 ? o[5][2 * h + e] : (cc == 2 ? o[9][2 * h + e] : o[13][2 * h + e]));
+          y.z = cc == 0 ? o[2][2 * h + e] : (cc == 1 ? o[6][2 * h + e] : (cc == 2 ? o[10][2 * h + e] : o[14][2 * h + e]));
+          y.w = cc == 0 ? o[3][2 * h + e] : (cc == 1 ? o[7][2 * h + e] : (cc == 2 ? o[11][2 * h + e] : o[15][2 * h + e]));
+          *reinterpret_cast<float4*>(dst + 16 * e + 4 * cc) = y;
+        }
+    }
+    __syncthreads();
+    const uint32_t bad = k4 ? 0u : poison;
+    const int r_lo = sp.i0 * pl.group, r_hi = min(sp.i1 * pl.group, R);
+    for (int r = r_lo + (tid >> 5); r < r_hi; r += kFewWarps) {        // a warp per row, 4 d's per lane
+      float m = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) {
+        const float2 v = ml_sm[w][r];
+        if (v.y != 0.f) m = fmaxf(m, v.x);
+      }
+      float L = 0.f;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) {
+        const float2 v = ml_sm[w][r];
+        if (v.y == 0.f) continue;                       // the row sees no key of this warp
+        const float a = ex2(v.x - m);
+        const float4 z = *reinterpret_cast<const float4*>(o_sm + ((size_t)w * kFewRows + r) * kOPitch + 4 * lane);
+        L += a * v.y;
+        y.x += a * z.x;
+        y.y += a * z.y;
+        y.z += a * z.z;
+        y.w += a * z.w;
+      }
+      const int p = n_past + r / pl.group, low = window_low(pl, p);
+      for (uint32_t left = bad; left; left &= left - 1) {
+        const int b = __ffs(left) - 1, t = b < 16 ? n_past + 1 + b : low0 + b - 16;
+        if (t > p || (t < low && t >= sinks)) continue;
+        const uint2 w = *reinterpret_cast<const uint2*>(vbase + (uint64_t)(uint32_t)page_at(kv, t >> 4) * stride + 256 * (t & 15) + 8 * lane);
+        const float v[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                            __uint_as_float(w.y & 0xFFFF0000u)};
+        if (!(fabsf(v[0]) <= 3.4e38f)) y.x += v[0];
+        if (!(fabsf(v[1]) <= 3.4e38f)) y.y += v[1];
+        if (!(fabsf(v[2]) <= 3.4e38f)) y.z += v[2];
+        if (!(fabsf(v[3]) <= 3.4e38f)) y.w += v[3];
+      }
+      const size_t at = ((size_t)slot * pl.nkv + kvh) * R + r;
+      reinterpret_cast<float4*>(part_o + at * 128)[lane] = y;
+      if (lane == 0) part_ml[at] = make_float2(m, L);
+    }
+    __syncthreads();                                    // the shared memory is free for the next pass
+  }
+}
+
+template <bool k4>
+static cudaError_t launch_few(const PattnPlan& pl, const KvView& kv, int layer, const float* q, float* part_o, float2* part_ml,
+                              cudaStream_t st) {
+  // the shared-memory limit is a per-device attribute
+  constexpr int kMaxDevices = 64;
+  static bool have[kMaxDevices] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < kMaxDevices;
+  if (!known || !have[dev]) {
+    e = cudaFuncSetAttribute(pattn_few_kernel<k4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSmem);
+    if (e != cudaSuccess) return e;
+    if (known) have[dev] = true;
+  }
+  pattn_few_kernel<k4><<<dim3(pl.slots, pl.nkv), 32 * kFewWarps, kFewSmem, st>>>(q, pl, kv, layer, part_o, part_ml);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pattn_few(bool k4, const PattnPlan& pl, const KvView& kv, int layer, const float* q, float* part_o,
+                             float2* part_ml, cudaStream_t st) {
+  return k4 ? launch_few<true>(pl, kv, layer, q, part_o, part_ml, st) : launch_few<false>(pl, kv, layer, q, part_o, part_ml, st);
+}
+
+}  // namespace spec

@@ -1,0 +1,110 @@
+// pattn_plan.cuh — how attention over a paged cache is cut into chunks of keys,
+// shared by its two kernels (pattn.cu, pattn_few.cu).
+#pragma once
+#include "common.cuh"
+#include "internal.h"
+
+namespace spec {
+
+constexpr int kKeys = 128;                          // keys of a tile
+constexpr int kPagesPerTile = kKeys / 16;
+
+struct PattnPlan {
+  int M, nq, nkv, group, window, sinks;
+  int C;                     // chunks of a KV head at most
+  unsigned long long c_inv;  // ceil(2^40 / C): t / C = t * c_inv >> 40 for t < 2^24
+  int slots;                 // chunk slots launched (<= C)
+  int Lw;                    // tiles per chunk at most (what the window needs)
+  int tile_rows;             // rows per row tile
+};
+
+// tiles per chunk of a row at position p
+SPEC_DEV int chunk_len(const PattnPlan& pl, int p) {
+  const int l = p > 0 ? (int)(((unsigned long long)(p >> 7) * pl.c_inv) >> 40) + 1 : 1;
+  return l < pl.Lw ? l : pl.Lw;
+}
+// the first position that a row at p sees through its window
+SPEC_DEV int window_low(const PattnPlan& pl, int p) { return pl.window > 0 && p >= pl.window ? p - pl.window + 1 : 0; }
+
+// x / d for 0 <= x < 2^24: the quotient in fp32 is off by less than one
+SPEC_DEV int div24(int x, int d) {
+  int q = (int)__fdividef((float)x, (float)d);
+  const int r = x - q * d;
+  return r < 0 ? q - 1 : (r >= d ? q + 1 : q);
+}
+
+// The rows of a block that share a chunk length (all of them, or the rows
+// before and after a step of chunk_len), and their chunk slots: the sinks'
+// chunks that end before the window, then the window's.
+struct Span {
+  int i0, i1;                // block rows [i0, i1)
+  int L, lo, last;           // tiles per chunk; first window key; last key
+  int sink_tiles, ns, cbase, nslots;
+};
+SPEC_DEV int span_count(const PattnPlan& pl, int n_past) {
+  return chunk_len(pl, n_past) == chunk_len(pl, n_past + pl.M - 1) ? 1 : 2;
+}
+SPEC_DEV Span span_of(const PattnPlan& pl, int n_past, int pass) {
+  Span s;
+  const int la = chunk_len(pl, n_past), lb = chunk_len(pl, n_past + pl.M - 1);
+  const int cut = la == lb ? pl.M : la * pl.C * kKeys - n_past;      // rows before the step
+  s.i0 = pass == 0 ? 0 : cut;
+  s.i1 = pass == 0 ? cut : pl.M;
+  s.L = pass == 0 ? la : lb;
+  s.lo = window_low(pl, n_past + s.i0);
+  s.last = n_past + s.i1 - 1;
+  s.sink_tiles = s.ns = s.cbase = s.nslots = 0;
+  if (s.last >= 0) {
+    const int sk = pl.window > 0 ? min(pl.sinks, s.last + 1) : 0;
+    s.sink_tiles = (int)(((unsigned)sk + kKeys - 1) / kKeys);
+    s.cbase = div24(s.lo >> 7, s.L);
+    s.ns = min(div24(s.sink_tiles + s.L - 1, s.L), s.cbase);
+    s.nslots = s.ns + div24(s.last >> 7, s.L) - s.cbase + 1;
+  }
+  return s;
+}
+// the key tiles of slot c: n0 from a0, then n - n0 from a1
+struct TileList {
+  int a0 = 0, n0 = 0, a1 = 0, n = 0;
+  SPEC_DEV int at(int j) const { return j < n0 ? a0 + j : a1 + (j - n0); }
+};
+SPEC_DEV TileList tiles_of(const Span& s, int c) {
+  TileList t;
+  if (c >= s.nslots) return t;
+  const int x = c < s.ns ? c : s.cbase + c - s.ns, from = x * s.L, to = from + s.L;
+  t.a0 = from;
+  t.n0 = max(0, min(to, s.sink_tiles) - from);
+  t.a1 = max(max(from, s.lo >> 7), from + t.n0);
+  t.n = t.n0 + max(0, min(to, (s.last >> 7) + 1) - t.a1);
+  return t;
+}
+
+SPEC_DEV uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
+
+// loads issued where they stand (a plain load may be moved down to its use,
+// behind a wait)
+SPEC_DEV uint4 ldg_now(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+SPEC_DEV uint32_t ldg_now(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u32 %0, [%1];\n" : "=r"(v) : "l"(p));
+  return v;
+}
+// the page id of a logical page, -1 past the table; to be checked where it is
+// used (a check here would wait for the load)
+SPEC_DEV int page_at(const KvView& kv, int lp) {
+  return lp < kv.max_seq_pages ? (int)ldg_now((const void*)(kv.page_table + lp)) : -1;
+}
+SPEC_DEV bool page_ok(const KvView& kv, int page) { return (uint32_t)page < (uint32_t)kv.num_pages; }
+
+// attention for a call of at most kFewRows query rows per KV head
+constexpr int kFewRows = 16;
+cudaError_t launch_pattn_few(bool k4, const PattnPlan& pl, const KvView& kv, int layer, const float* q, float* part_o,
+                             float2* part_ml, cudaStream_t st);
+
+}  // namespace spec

@@ -420,38 +420,50 @@ def test_attention_bf16_values_past_binary16(M, window, sinks):
     assert status(ctx) == 0
 
 
+# the kinds of calls within which a row has the same bits: at most 16 query rows
+# per KV head, one tile of 128 of them, two; each with blocks (first row, rows)
+BLOCKS = {"few": (16, 16, 16, ((0, 1), (0, 4), (7, 1), (15, 1), (8, 8), (5, 7))),
+          "few_grouped": (4, 8, 2, ((0, 1), (3, 1), (1, 2), (1, 3))),
+          "tile": (9, 26, 2, ((0, 2), (0, 4), (7, 2), (1, 8), (5, 3))),
+          "two_tiles": (16, 26, 2, ((0, 10), (0, 13), (6, 10), (1, 15), (2, 12)))}
+
+
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("blocks", sorted(BLOCKS))
 @pytest.mark.parametrize("n_past,window,sinks", [(45, 0, 0), (1000, 0, 0), (1000, 200, 9), (120, 121, 2)])
-def test_attention_batch_height_invariance(kind, n_past, window, sinks):
-    """A row has the same bits alone and in every block that places it there."""
-    ctx = context(26, 2)
-    M = 16
+def test_attention_batch_height_invariance(kind, n_past, window, sinks, blocks):
+    """A row has the same bits in every block of a kind that places it there."""
+    M, nq, nkv, parts = BLOCKS[blocks]
+    ctx = context(nq, nkv)
     kv, _, _, _ = cache(ctx, kind, n_past + M, 31)
-    q = np.random.default_rng(5).standard_normal((M, 26, 128)).astype(np.float32) * 3
+    q = np.random.default_rng(5).standard_normal((M, nq, 128)).astype(np.float32) * 3
     whole = attend(ctx, kv, kind, q, window, sinks)
-    for i, m in ((0, 1), (3, 4), (7, 1), (15, 1), (15, 8), (11, 7)):
-        kv.seq_len[0] = n_past + i + 1
-        part = attend(ctx, kv, kind, q[i - m + 1:i + 1], window, sinks)
-        assert np.array_equal(part.view(np.uint32), whole[i - m + 1:i + 1].view(np.uint32)), (i, m)
+    for i, m in parts:
+        kv.seq_len[0] = n_past + i + m
+        part = attend(ctx, kv, kind, q[i:i + m], window, sinks)
+        assert np.array_equal(part.view(np.uint32), whole[i:i + m].view(np.uint32)), (i, m)
 
 
 @pytest.mark.parametrize("kind", KINDS)
-def test_attention_across_a_chunk_size_step(kind):
+@pytest.mark.parametrize("nq,m", [(64, 1), (128, 9)])
+def test_attention_across_a_chunk_size_step(kind, nq, m):
     """Blocks around every length at which the kernels change their split of the
-    keys: right, and the same bits for a row alone."""
-    ctx = context(64, 64, max_ctx=4096)
+    keys: right, and the same bits in a smaller block."""
+    ctx = context(nq, 64, max_ctx=4096)
     kv, k, v, _ = cache(ctx, kind, 1100, 41)
-    q = np.random.default_rng(5).standard_normal((16, 64, 128)).astype(np.float32)
+    q = np.random.default_rng(5).standard_normal((16, nq, 128)).astype(np.float32)
     for boundary in (256, 512, 768, 1024):
         for length in (boundary + 5, boundary + 16, boundary):
             kv.seq_len[0] = length
             whole = attend(ctx, kv, kind, q, 0, 0)
-            want, bound = u.attention(q, k, v, 64, 0, 0, length, split=SPLIT[kind])
+            want, bound = u.attention(q, k, v, nq, 0, 0, length, split=SPLIT[kind])
             assert (np.abs(whole - want) <= bound).all()
-            for i in (0, 9, 10, 11, 15):
-                kv.seq_len[0] = length - 15 + i
-                part = attend(ctx, kv, kind, q[i:i + 1], 0, 0)
-                assert np.array_equal(part.view(np.uint32), whole[i:i + 1].view(np.uint32)), (length, i)
+            for i in (0, 1, 4, 6, 7, 9, 10, 11, 15):
+                if i + m > 16:
+                    continue
+                kv.seq_len[0] = length - 16 + i + m
+                part = attend(ctx, kv, kind, q[i:i + m], 0, 0)
+                assert np.array_equal(part.view(np.uint32), whole[i:i + m].view(np.uint32)), (length, i)
 
 
 @pytest.mark.parametrize("kind", KINDS)
