@@ -1,8 +1,10 @@
 // kv4.cu — writing and reading the rows of a 4-bit KV cache (page layout and
 // arithmetic: kv4.cuh).
 //
-// Both kernels move one pass over their data: 4 bytes per value on the fp32
-// side and 9/16 on the paged side, so they are bound by memory traffic.
+// Both kernels make one pass over their data: 4 bytes per value on the fp32
+// side and 9/16 on the paged side, so they are bound by memory traffic.  A CTA
+// takes the 16 positions of one page and KV head, K and V, so that the pages are
+// written and read whole.
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.cuh"
@@ -11,107 +13,152 @@ namespace spec {
 
 constexpr int kKv4Threads = 256;
 
-// the page of (lp, layer, which, head), nullptr when lp is not mapped
-SPEC_DEV uint8_t* kv4_page(const KvView& kv, int lp, int layer, int which, int head) {
+// the K page of (lp, layer, head), nullptr when lp is not mapped; V's is
+// n_kv pages behind it
+SPEC_DEV uint8_t* kv4_page(const KvView& kv, int lp, int layer, int head) {
   if (lp < 0 || lp >= kv.max_seq_pages) return nullptr;
   const int page = kv.page_table[lp];
   if (page < 0 || page >= kv.num_pages) return nullptr;
   return reinterpret_cast<uint8_t*>(kv.pool) +
-         ((((size_t)page * kv.n_layers + layer) * 2 + which) * kv.n_kv + head) * kKv4PageBytes;
+         (((size_t)page * kv.n_layers + layer) * 2 * kv.n_kv + head) * kKv4PageBytes;
 }
 
-// 16 lanes per (row, K or V, head), 8 values each; two lanes share a group of
-// 16 and its scale.
+// 16 lanes per position, 8 values of K and 8 of V each; two lanes share a group
+// of 16 and its scale.
+//
+// The code of x under scale s is the e2m1 number nearest to x / s, ties to the
+// even code.  x (1/s) in fp32 is off by less than 2^-22 of itself.  The
+// conversion is monotone, so where x (1/s) (1 - 2^-20) and x (1/s) (1 + 2^-20)
+// have the same code it is that of x / s; where they differ x / s is next to a
+// tie, and the comparisons of kv4_code decide.
 __global__ void __launch_bounds__(kKv4Threads)
 kv4_append_kernel(const float* __restrict__ k, const float* __restrict__ v, long long ld, int n, KvView kv, int layer,
                   int32_t* status) {
   pdl_trigger();
+  const uint32_t tile = blockIdx.x / (uint32_t)kv.n_kv, head = blockIdx.x - tile * kv.n_kv;
+  const int sub = threadIdx.x & 15, t = threadIdx.x >> 4;
   pdl_wait();
-  const int sub = threadIdx.x & 15;
-  const long long item = ((long long)blockIdx.x * kKv4Threads + threadIdx.x) >> 4;
-  const int per_row = 2 * kv.n_kv;
-  const int row = (int)(item / per_row), rest = (int)(item % per_row);
-  const bool in = row < n;
-  const int which = rest / kv.n_kv, head = rest % kv.n_kv;
-  float x[8] = {};
-  if (in) {
-    const float* src = (which ? v : k) + (size_t)row * ld + head * 128 + 8 * sub;
-    const float4 a = reinterpret_cast<const float4*>(src)[0], b = reinterpret_cast<const float4*>(src)[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  }
-  float amax = 0.f;
-  bool bad = false;
+  const long long pos0 = (long long)*kv.seq_len - n;    // may lie below 0
+  const long long lp = (pos0 >> 4) + tile, pos = lp * 16 + t, row = pos - pos0;
+  const bool in = row >= 0 && row < n;
+  float x[2][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    bad = bad || !(fabsf(x[i]) <= 3.40282347e38f);
-    if (x[i] != x[i]) x[i] = 0.f;                    // a NaN is stored as 0
-    amax = fmaxf(amax, fabsf(x[i]));
+  for (int which = 0; which < 2; ++which) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    if (in) {
+      const float* src = (which ? v : k) + (size_t)row * ld + head * 128 + 8 * sub;
+      a = reinterpret_cast<const float4*>(src)[0];
+      b = reinterpret_cast<const float4*>(src)[1];
+    }
+    x[which][0] = a.x; x[which][1] = a.y; x[which][2] = a.z; x[which][3] = a.w;
+    x[which][4] = b.x; x[which][5] = b.y; x[which][6] = b.z; x[which][7] = b.w;
   }
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  if (!in) return;
-  if (bad) atomicOr(status, SPEC_ST_NONFINITE);
-  const int pos = *kv.seq_len - n + row;
-  uint8_t* pg = pos >= 0 ? kv4_page(kv, pos >> 4, layer, which, head) : nullptr;
-  if (!pg) {
-    if (sub == 0) atomicOr(status, SPEC_ST_CTX_FULL);
-    return;
-  }
-  const uint32_t sb = kv4_scale_byte(amax);
-  const float s = kv4_scale(sb);
-  uint32_t w = 0;
+  uint8_t* pg = lp >= 0 && lp < kv.max_seq_pages ? kv4_page(kv, (int)lp, layer, head) : nullptr;
+  if (in && !pg && sub == 0) atomicOr(status, SPEC_ST_CTX_FULL);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w |= (sb ? kv4_code(x[i], s) : (__float_as_uint(x[i]) >> 28) & 8u) << (4 * i);
-  const int t = pos & 15;
-  *reinterpret_cast<uint32_t*>(pg + kv4_chunk(t, sub >> 2) + 4 * (sub & 3)) = w;
-  if ((sub & 1) == 0) pg[kKv4Scales + 8 * t + (sub >> 1)] = (uint8_t)sb;
+  for (int which = 0; which < 2; ++which) {
+    float (&y)[8] = x[which];
+    float amax = 0.f;                                   // NaN if there is one
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;\n" : "+f"(amax) : "f"(fabsf(y[i])));
+    const bool bad = !(amax <= 3.40282347e38f);
+    if (bad) {
+      atomicOr(status, SPEC_ST_NONFINITE);
+      amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (y[i] != y[i]) y[i] = 0.f;                   // a NaN is stored as 0
+        amax = fmaxf(amax, fabsf(y[i]));
+      }
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    const uint32_t sb = kv4_scale_byte(amax);
+    const float s = kv4_scale(sb), inv = 1.0f / s;
+    const float up = inv * (1.f + 0x1p-20f), down = inv * (1.f - 0x1p-20f);
+    float y0[8], y1[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      y0[i] = y[i] * down;
+      y1[i] = y[i] * up;
+    }
+    uint32_t w = e2m1_word(y0);
+    if (w != e2m1_word(y1) || sb == 0) {
+      w = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w |= (sb ? kv4_code(y[i], s) : (__float_as_uint(y[i]) >> 28) & 8u) << (4 * i);
+    }
+    if (in && pg) {
+      uint8_t* dst = pg + (which ? (size_t)kv.n_kv * kKv4PageBytes : 0);
+      *reinterpret_cast<uint32_t*>(dst + kv4_chunk(t, sub >> 2) + 4 * (sub & 3)) = w;
+      if ((sub & 1) == 0) dst[kKv4Scales + 8 * t + (sub >> 1)] = (uint8_t)sb;
+    }
+  }
 }
 
+// A warp per position, K then V, 4 values per lane, so that a store is a whole
+// row of 512 bytes; all of a lane's loads come before its first store.
 __global__ void __launch_bounds__(kKv4Threads)
 kv4_read_kernel(KvView kv, int layer, int pos0, int n, float* __restrict__ k, float* __restrict__ v, long long ld) {
   pdl_trigger();
+  const uint32_t tile = blockIdx.x / (uint32_t)kv.n_kv, head = blockIdx.x - tile * kv.n_kv;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kWarps = kKv4Threads / 32, kRows = 16 / kWarps;
+  const long long lp = (pos0 >> 4) + tile;
   pdl_wait();
-  const int sub = threadIdx.x & 15;
-  const long long item = ((long long)blockIdx.x * kKv4Threads + threadIdx.x) >> 4;
-  const int per_row = 2 * kv.n_kv;
-  const int row = (int)(item / per_row), rest = (int)(item % per_row);
-  if (row >= n) return;
-  const int which = rest / kv.n_kv, head = rest % kv.n_kv;
-  const int pos = pos0 + row, t = pos & 15;
-  const uint8_t* pg = pos < *kv.seq_len ? kv4_page(kv, pos >> 4, layer, which, head) : nullptr;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-  if (pg) {
-    uint32_t c[4];
-    e2m1_word(*reinterpret_cast<const uint32_t*>(pg + kv4_chunk(t, sub >> 2) + 4 * (sub & 3)), c);
-    const float s = kv4_scale(pg[kKv4Scales + 8 * t + (sub >> 1)]);
-    float y[8];
+  const int seq_len = *kv.seq_len;
+  const uint8_t* pg = lp < kv.max_seq_pages ? kv4_page(kv, (int)lp, layer, head) : nullptr;
+  uint32_t code[kRows][2], sb[kRows][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&c[i]));
-      y[2 * i] = f.x * s;
-      y[2 * i + 1] = f.y * s;
+  for (int r = 0; r < kRows; ++r) {
+    const int t = warp + kWarps * r;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      code[r][which] = sb[r][which] = 0;
+      if (pg && lp * 16 + t < seq_len) {
+        const uint8_t* src = pg + (which ? (size_t)kv.n_kv * kKv4PageBytes : 0);
+        code[r][which] = *reinterpret_cast<const uint16_t*>(src + kv4_chunk(t, lane >> 3) + 2 * (lane & 7));
+        sb[r][which] = src[kKv4Scales + 8 * t + (lane >> 2)];
+      }
     }
-    a = make_float4(y[0], y[1], y[2], y[3]);
-    b = make_float4(y[4], y[5], y[6], y[7]);
   }
-  float4* dst = reinterpret_cast<float4*>((which ? v : k) + (size_t)row * ld + head * 128 + 8 * sub);
-  dst[0] = a;
-  dst[1] = b;
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    const long long row = lp * 16 + warp + kWarps * r - pos0;
+    if (row < 0 || row >= n) continue;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      uint32_t f0, f1;
+      e2m1_pairs(code[r][which], f0, f1);
+      const uint32_t s2 = min(sb[r][which], (uint32_t)kKv4TopScale) * 0x00800080u;      // the scale in both halves
+      f0 = hmul2_u32(f0, s2);
+      f1 = hmul2_u32(f1, s2);
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&f0));
+      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&f1));
+      *reinterpret_cast<float4*>((which ? v : k) + (size_t)row * ld + head * 128 + 4 * lane) = make_float4(a.x, a.y, b.x, b.y);
+    }
+  }
 }
 
-static unsigned kv4_grid(const KvView& kv, int n) {
-  return (unsigned)(((long long)n * 2 * kv.n_kv * 16 + kKv4Threads - 1) / kKv4Threads);
+// pages that n rows can touch
+static long long kv4_tiles(int n) { return ((long long)n + 15) / 16 + 1; }
+static bool kv4_grid(const KvView& kv, long long tiles, unsigned& grid) {
+  grid = (unsigned)(tiles * kv.n_kv);
+  return tiles * kv.n_kv <= 0x7FFFFFFFll;
 }
 
 cudaError_t launch_kv4_append(const float* k, const float* v, int ld, int n, const KvView& kv, int layer,
                               int32_t* status, cudaStream_t st) {
-  kv4_append_kernel<<<kv4_grid(kv, n), kKv4Threads, 0, st>>>(k, v, ld, n, kv, layer, status);
+  unsigned grid;
+  if (!kv4_grid(kv, kv4_tiles(n), grid)) return cudaErrorInvalidConfiguration;
+  kv4_append_kernel<<<grid, kKv4Threads, 0, st>>>(k, v, ld, n, kv, layer, status);
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv4_read(const KvView& kv, int layer, int pos0, int n, float* k, float* v, int ld,
                             cudaStream_t st) {
-  kv4_read_kernel<<<kv4_grid(kv, n), kKv4Threads, 0, st>>>(kv, layer, pos0, n, k, v, ld);
+  unsigned grid;
+  if (!kv4_grid(kv, ((long long)pos0 + n + 15) / 16 - pos0 / 16, grid)) return cudaErrorInvalidConfiguration;
+  kv4_read_kernel<<<grid, kKv4Threads, 0, st>>>(kv, layer, pos0, n, k, v, ld);
   return cudaGetLastError();
 }
 

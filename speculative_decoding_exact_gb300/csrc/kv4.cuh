@@ -28,21 +28,24 @@ SPEC_DEV float kv4_scale(uint32_t byte) {
 }
 
 // the smallest scale byte whose scale s has 6 s >= amax (the top one if none
-// has): truncating amax / 6 to 5 + 3 bits lands on it or next to it, and 6 s is
-// exact in fp32, so the two comparisons settle it
+// has): amax / 6 truncated to 5 + 3 bits, or the byte after it.  6 s is exact in
+// fp32, so the comparison settles which.
 SPEC_DEV uint32_t kv4_scale_byte(float amax) {
   if (!(amax <= 6.f * 10240.f)) return kKv4TopScale;
-  int b = __half_as_ushort(__float2half_rz(amax * (1.0f / 6.0f))) >> 7;
-  while (b < kKv4TopScale && 6.f * kv4_scale(b) < amax) ++b;
-  while (b > 0 && 6.f * kv4_scale(b - 1) >= amax) --b;
-  return (uint32_t)b;
+  const uint32_t b = __half_as_ushort(__float2half_rz(amax * (1.0f / 6.0f))) >> 7;
+  return 6.f * kv4_scale(b) < amax ? b + 1 : b;
 }
 
-// two e2m1 codes of y0 (low nibble) and y1, nearest with ties to even
-SPEC_DEV uint32_t e2m1x2(float y0, float y1) {
-  uint32_t r;
-  asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n cvt.u32.u8 %0, t;\n}\n" : "=r"(r) : "f"(y1), "f"(y0));
-  return r;
+// the codes nearest to 8 values, element i in nibble i
+SPEC_DEV uint32_t e2m1_word(const float (&y)[8]) {
+  uint32_t w;
+  asm("{\n .reg .b8 a, b, c, d;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      " mov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(w)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+  return w;
 }
 // the 8 codes of a word as f16 pairs, element 2i in the low half of out[i]
 SPEC_DEV void e2m1_word(uint32_t w, uint32_t (&out)[4]) {
@@ -50,6 +53,13 @@ SPEC_DEV void e2m1_word(uint32_t w, uint32_t (&out)[4]) {
       " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
       " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
       : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3])
+      : "r"(w));
+}
+// the 4 codes of 16 bits as f16 pairs
+SPEC_DEV void e2m1_pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %2;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n}\n"
+      : "=r"(lo), "=r"(hi)
       : "r"(w));
 }
 SPEC_DEV uint32_t hmul2_u32(uint32_t a, uint32_t b) {
