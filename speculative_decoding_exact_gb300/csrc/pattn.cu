@@ -713,13 +713,14 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
       const size_t at = ((size_t)slot * pl.nkv + kvh) * R + fr;
       if (mine) {
         if (h == 0) part_ml[at] = make_float2(ref - kBias, lsum + pair[1][r]);
-        float4* dst = reinterpret_cast<float4*>(part_o + at * 128 + 64 * h);
+        // [slot][KV head][d / 4][row]: a warp's rows side by side
+        float4* dst = reinterpret_cast<float4*>(part_o) + (((size_t)slot * pl.nkv + kvh) * 32 + 16 * h) * R + fr;
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
           float4 y;
           f2unpack(acc[2 * c], y.x, y.y);
           f2unpack(acc[2 * c + 1], y.z, y.w);
-          dst[c] = y;
+          dst[(size_t)c * R] = y;
         }
       }
       named_bar(1 + ww, 64);                            // `pair` is free
@@ -736,58 +737,96 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
 }
 
 // ---------------------------------------------------------------------------
-// merge: one warp per (row, head), 4 output elements per lane.  With m the
-// largest chunk maximum (base 2) and w_c = 2^(m_c - m):
-//   out = sum_c w_c o_c / sum_c w_c l_c, both in chunk order over the chunks in
-// which the row sees a key, so the order does not depend on the block.
+// merge: four threads per 4 output elements, one per residue of the chunk number
+// mod 4; a warp takes 32 neighbouring rows, which lie side by side in the
+// partials.  With m the largest chunk maximum (base 2) and w_c = 2^(m_c - m):
+//   out = sum_c w_c o_c / sum_c w_c l_c, over the chunks in which the row sees a
+// key, first within each residue in chunk order, then over the residues, so the
+// order does not depend on the block.
 // ---------------------------------------------------------------------------
-constexpr int kMergeWarps = 4;
+constexpr int kMergeParts = 4;
 
-__global__ void __launch_bounds__(32 * kMergeWarps)
-pattn_merge_kernel(const float* __restrict__ part_o, const float2* __restrict__ part_ml, PattnPlan pl,
-                   const int32_t* __restrict__ seq_len, float* __restrict__ out) {
+__global__ void __launch_bounds__(32 * kMergeParts)
+pattn_merge_kernel(const float4* __restrict__ part_o, const float2* __restrict__ part_ml, PattnPlan pl,
+                   const int32_t* __restrict__ seq_len, float4* __restrict__ out) {
+  __shared__ float4 o_sm[kMergeParts][32];
+  __shared__ float2 ml_sm[kMergeParts][32];
   pdl_trigger();
-  const int item = blockIdx.x * kMergeWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int i = div24(item, pl.nq), head = item - i * pl.nq, kvh = div24(head, pl.group);
+  const int lane = threadIdx.x & 31, res = threadIdx.x >> 5;
+  const int R = pl.M * pl.group, item = blockIdx.x * 32 + lane;       // ((KV head, d / 4), row); a grid of whole warps
+  const int hd = div24(item, R), r = item - hd * R, kvh = hd >> 5, d4 = hd & 31;
+  const int i = div24(r, pl.group), head = kvh * pl.group + r - i * pl.group;
   pdl_wait();
-  if (item >= pl.M * pl.nq) return;
   const int n_past = __ldcg(seq_len) - pl.M;
   Span s = span_of(pl, n_past, 0);
   if (i >= s.i1) s = span_of(pl, n_past, 1);
-  const int n = n_past + i < 0 ? 0 : min(s.nslots, pl.slots);
-  const size_t stride = (size_t)pl.nkv * pl.M * pl.group;
-  const size_t at = (size_t)kvh * pl.M * pl.group + i * pl.group + (head - kvh * pl.group);
-  float m = -INFINITY;
-  for (int c = lane; c < n; c += 32) {
-    const float2 x = __ldcg(part_ml + at + c * stride);
-    if (x.y != 0.f) m = fmaxf(m, x.x);
-  }
+  const int slots = n_past + i < 0 ? 0 : min(s.nslots, pl.slots);
+  // this residue's slots: n0 of the sinks' from slot res on, then those from c1 on
+  const int ns = min(s.ns, slots), n0 = (ns + kMergeParts - 1 - res) / kMergeParts;
+  const int c1 = ns + ((res - s.cbase) & (kMergeParts - 1));
+  const int n = n0 + max(0, slots - c1 + kMergeParts - 1) / kMergeParts;
+  auto slot = [&](int j) { return j < n0 ? res + kMergeParts * j : c1 + kMergeParts * (j - n0); };
+  const size_t step = (size_t)pl.nkv * R, at = (size_t)kvh * R + r;
+  const float4* po = part_o + (size_t)hd * R + r;
+  constexpr int kBatch = 8;                             // loads in flight
+  float m = -INFINITY, L = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float L = 0.f;
-  constexpr int kBatch = 16;                            // loads in flight
-  for (int c0 = 0; c0 < n; c0 += kBatch) {
+  for (int j0 = 0; j0 < n; j0 += kBatch) {
     float4 y[kBatch];
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k)
-      if (c0 + k < n) y[k] = __ldcg(reinterpret_cast<const float4*>(part_o + (at + (c0 + k) * stride) * 128) + lane);
-    const float2 x = lane < kBatch && c0 + lane < n ? __ldcg(part_ml + at + (c0 + lane) * stride) : make_float2(0.f, 0.f);
-    if (c0 == 0) m = warp_max(m);
-    const float wl = x.y != 0.f ? exp2f(x.x - m) : 0.f;
+    float2 x[kBatch];
+    float top = m;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const float w = __shfl_sync(0xffffffffu, wl, k), l = __shfl_sync(0xffffffffu, x.y, k);
-      if (c0 + k < n && l != 0.f) {
-        L += w * l;
+      x[k] = make_float2(0.f, 0.f);
+      if (j0 + k < n) {
+        const size_t c = slot(j0 + k);
+        x[k] = __ldcg(part_ml + at + c * step);
+        y[k] = __ldcg(po + 32 * c * step);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (x[k].y != 0.f) top = fmaxf(top, x[k].x);
+    if (top > m) {
+      const float a = exp2f(m - top);
+      m = top;
+      L *= a;
+      o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (x[k].y != 0.f) {
+        const float w = exp2f(x[k].x - m);
+        L += w * x[k].y;
         o.x += w * y[k].x;
         o.y += w * y[k].y;
         o.z += w * y[k].z;
         o.w += w * y[k].w;
       }
-    }
   }
-  const bool none = L == 0.f;                          // nothing visible: zero
-  reinterpret_cast<float4*>(out + ((size_t)i * pl.nq + head) * 128)[lane] =
-      none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x / L, o.y / L, o.z / L, o.w / L);
+  o_sm[res][lane] = o;
+  ml_sm[res][lane] = make_float2(m, L);
+  __syncthreads();
+  if (res != 0) return;
+  m = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kMergeParts; ++k) m = fmaxf(m, ml_sm[k][lane].x);
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+  L = 0.f;
+#pragma unroll
+  for (int k = 0; k < kMergeParts; ++k) {
+    const float2 x = ml_sm[k][lane];
+    if (x.y == 0.f) continue;
+    const float w = exp2f(x.x - m);
+    const float4 y = o_sm[k][lane];
+    L += w * x.y;
+    o.x += w * y.x;
+    o.y += w * y.y;
+    o.z += w * y.z;
+    o.w += w * y.w;
+  }
+  out[((size_t)i * pl.nq + head) * 32 + d4] =           // nothing visible: zero
+      L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x / L, o.y / L, o.z / L, o.w / L);
 }
 
 // chunks of a KV head at most: one per SM, KV head and row tile, so that the
@@ -860,13 +899,13 @@ cudaError_t launch_paged_attention(bool k4, const KvView& kv, int layer, const f
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((M * nq + kMergeWarps - 1) / kMergeWarps);
-  cfg.blockDim = dim3(32 * kMergeWarps);
+  cfg.gridDim = dim3(M * nq);
+  cfg.blockDim = dim3(32 * kMergeParts);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, pattn_merge_kernel, (const float*)po, (const float2*)ml, pl,
-                            (const int32_t*)kv.seq_len, out);
+  return cudaLaunchKernelEx(&cfg, pattn_merge_kernel, reinterpret_cast<const float4*>(po), (const float2*)ml, pl,
+                            (const int32_t*)kv.seq_len, reinterpret_cast<float4*>(out));
 }
 
 }  // namespace spec

@@ -485,7 +485,7 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
         if (!(fabsf(v[3]) <= 3.4e38f)) y.w += v[3];
       }
       const size_t at = ((size_t)slot * pl.nkv + kvh) * R + r;
-      reinterpret_cast<float4*>(part_o + at * 128)[lane] = y;
+      reinterpret_cast<float4*>(part_o)[(((size_t)slot * pl.nkv + kvh) * 32 + lane) * R + r] = y;
       if (lane == 0) part_ml[at] = make_float2(m, L);
     }
     __syncthreads();                                    // the shared memory is free for the next pass
