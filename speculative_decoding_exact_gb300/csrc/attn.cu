@@ -118,20 +118,11 @@ size_t attn_partial_floats(const AttnPlan& a, int max_rows) {
   return (size_t)a.max_chunks * a.nq * 16 * kPartStride;
 }
 
-// 2-D tensor copy global -> shared: box at (x, y) of the map, completion on mbar
-SPEC_DEV void tma_load_2d(void* dst_smem, const CUtensorMap* map, int x, int y, uint64_t* mbar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
-          smem_u32(dst_smem)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(mbar))
-      : "memory");
-}
-
 // The KV pool [num_pages][n_layers][K, V][n_kv][16 positions][128] bf16 seen as
 // one 2-D tensor of 256-byte rows (row = ((page*n_layers + layer)*2 + kv)*n_kv
 // + head, times 16, plus the position in the page); boxes of 16 rows x 64
 // values (one d half of one page), 128-byte swizzle.
-static cudaError_t make_kv_tmap(const KvView& kv, CUtensorMap* map) {
+cudaError_t make_kv_tmap(const KvView& kv, CUtensorMap* map) {
   using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);

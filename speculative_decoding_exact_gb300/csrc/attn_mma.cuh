@@ -1,7 +1,11 @@
 // attn_mma.cuh — what the attention kernels share: tensor-memory loads, operand
-// descriptors, the shared-memory MMA and the base-2 exponential.
+// descriptors, the shared-memory MMA, the copies of K and V and the base-2
+// exponential.
 #pragma once
+#include <cuda.h>
+
 #include "common.cuh"
+#include "internal.h"
 
 namespace spec {
 
@@ -32,5 +36,17 @@ SPEC_DEV void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint
       " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
 }
+
+// 2-D tensor copy global -> shared: box at (x, y) of the map, completion on mbar
+SPEC_DEV void tma_load_2d(void* dst_smem, const CUtensorMap* map, int x, int y, uint64_t* mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
+          smem_u32(dst_smem)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(mbar))
+      : "memory");
+}
+
+// tensor map of the KV pool: one d half of a page per box (attn.cu)
+cudaError_t make_kv_tmap(const KvView& kv, CUtensorMap* map);
 
 }  // namespace spec

@@ -43,7 +43,6 @@ namespace spec {
 
 constexpr int kHalf = kKeys * 128;                  // one d half of a K or V tile: [keys][64 values]
 constexpr int kStageBytes = 4 * kHalf;              // K then V, 64 KB
-constexpr uint64_t kPattnWaitNs = 2000000000ull;
 
 constexpr int kStages = 3;                          // [d half][key][128 B], 128-byte swizzle; K, then V
 constexpr size_t kPattnSmem = 1024 + (size_t)kStages * kStageBytes;
@@ -86,36 +85,6 @@ SPEC_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
           taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
-}
-
-SPEC_DEV void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
-}
-
-// wait for a phase, giving up after kPattnWaitNs
-SPEC_DEV bool mbar_wait(uint64_t* mbar, uint32_t parity) {
-#pragma unroll 1
-  for (int i = 0; i < 64; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(smem_u32(mbar)), "r"(parity)
-        : "memory");
-    if (done) return true;
-  }
-  return mbar_wait_ns(mbar, parity, kPattnWaitNs);
-}
-SPEC_DEV void named_bar(int id, int count) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(count) : "memory"); }
-SPEC_DEV bool named_bar_or(int id, int count, bool pred) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"((uint32_t)pred), "r"(id), "r"(count)
-      : "memory");
-  return r != 0;
 }
 
 // One page of a tile as an unpacking warp holds it.
@@ -893,7 +862,7 @@ cudaError_t launch_paged_attention(bool k4, const KvView& kv, int layer, const f
   float* po = part + 2 * (size_t)pl.C * nq * 16;
   cudaError_t e = R <= kFewRows ? launch_pattn_few(k4, pl, kv, layer, q, po, ml, st)
                   : k4          ? launch_pattn<true>(pl, kv, layer, q, row_tiles, po, ml, status, st)
-                                : launch_pattn<false>(pl, kv, layer, q, row_tiles, po, ml, status, st);
+                                : launch_pattn_bf16(pl, kv, layer, q, row_tiles, po, ml, status, st);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -102,9 +102,44 @@ SPEC_DEV int page_at(const KvView& kv, int lp) {
 }
 SPEC_DEV bool page_ok(const KvView& kv, int page) { return (uint32_t)page < (uint32_t)kv.num_pages; }
 
+constexpr uint64_t kPattnWaitNs = 2000000000ull;
+SPEC_DEV void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
+}
+
+// wait for a phase, giving up after kPattnWaitNs
+SPEC_DEV bool mbar_wait(uint64_t* mbar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(smem_u32(mbar)), "r"(parity)
+        : "memory");
+    if (done) return true;
+  }
+  return mbar_wait_ns(mbar, parity, kPattnWaitNs);
+}
+SPEC_DEV void named_bar(int id, int count) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(count) : "memory"); }
+SPEC_DEV bool named_bar_or(int id, int count, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)pred), "r"(id), "r"(count)
+      : "memory");
+  return r != 0;
+}
+
 // attention for a call of at most kFewRows query rows per KV head
 constexpr int kFewRows = 16;
 cudaError_t launch_pattn_few(bool k4, const PattnPlan& pl, const KvView& kv, int layer, const float* q, float* part_o,
                              float2* part_ml, cudaStream_t st);
+
+// attention over a bf16 cache for more rows
+cudaError_t launch_pattn_bf16(const PattnPlan& pl, const KvView& kv, int layer, const float* q, int row_tiles, float* part_o,
+                              float2* part_ml, int32_t* status, cudaStream_t st);
 
 }  // namespace spec
