@@ -48,6 +48,12 @@ SPEC_DEV uint32_t take_bf16(float& x0, float& x1) {
   x1 -= __uint_as_float(b & 0xFFFF0000u);
   return __byte_perm(a, b, 0x7632);
 }
+// one TMEM column (to be waited for)
+SPEC_DEV uint32_t tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n" : "=r"(r) : "r"(taddr));
+  return r;
+}
 // an element of a bf16 pair is infinite or NaN
 SPEC_DEV bool nonfinite(uint32_t w) { return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u; }
 
@@ -119,11 +125,11 @@ pattn_bf16_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, const __
 
   // one tile's K (V) pages; lane l < 16 copies d half l % 2 of page l / 2.  An
   // unmapped page is a box outside the tensor, which reads as zeros.
-  auto issue = [&](int it, bool is_v) {
+  auto page_of = [&](int it) { return it < total ? page_at(kv, tile_at(it) * kPagesPerTile + ((lane >> 1) & 7)) : -1; };
+  auto issue = [&](int it, bool is_v, int page) {
     const int st = it % kStages;
     uint64_t* full = is_v ? &v_here[st] : &k_full[st];
     const int pp = (lane >> 1) & 7, half = lane & 1;
-    const int page = page_at(kv, tile_at(it) * kPagesPerTile + pp);
     const bool ok = page_ok(kv, page);
     if (!is_v && lane < 16 && half == 0) mapped[it & 7][pp] = ok;
     __syncwarp();
@@ -133,8 +139,15 @@ pattn_bf16_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, const __
       tma_load_2d(stages + st * kStageBytes + (is_v ? 2 : 0) * kHalf + half * kHalf + pp * 2048, &map, 64 * half,
                   ok ? (((page * kv.n_layers + layer) * 2 + is_v) * kv.n_kv + kvh) * 16 : -16, full);
   };
+  int next_page = -1;                                   // of a copying warp: the ids of its next tile
   if (warp == kWLoadK || warp == kWLoadV) {
-    for (int it = 0; it < kStages && it < total; ++it) issue(it, warp == kWLoadV);
+    int ids[kStages];
+#pragma unroll
+    for (int it = 0; it < kStages; ++it) ids[it] = page_of(it);
+    next_page = page_of(kStages);
+#pragma unroll
+    for (int it = 0; it < kStages; ++it)
+      if (it < total) issue(it, warp == kWLoadV, ids[it]);
   } else if (total > 0) {
 #pragma unroll
     for (int j = 0; j < kQRows; ++j) {
@@ -227,7 +240,9 @@ pattn_bf16_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, const __
     for (; ok && it < total; ++it) {
       ok = __all_sync(0xffffffffu, mbar_wait(is_v ? &v_free[it % kStages] : &k_free[it % kStages], ((it / kStages) - 1) & 1));
       if (!ok) break;
-      issue(it, is_v);
+      const int page = next_page;
+      next_page = page_of(it + 1);
+      issue(it, is_v, page);
     }
     // no copy is in flight when the CTA ends
     const int issued = min(it, total);
@@ -361,19 +376,13 @@ pattn_bf16_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, const __
 #pragma unroll
         for (int e = 0; e < 64; ++e) m4[e & 3] = fmaxf(m4[e & 3], x[e]);
         float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * unit;
-        // V has been looked through
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&v_full[st], (it / kStages) & 1));
-        const uint4 far = *reinterpret_cast<const uint4*>(&odd[it & 7][0]);
-        const bool any_far = (far.x | far.y | far.z | far.w) != 0;
         // The reference moves only when a score exceeds it by more than 8.  A wait
         // that ran out is carried to this barrier, where the pair of warps leaves
         // together.
         if (!ok) *reinterpret_cast<volatile int*>(&gave_up[ww]) = 1;
-        bool special = false;
-        if (named_bar_or(1 + ww, 64, mx > ref + 8.f || !ok || any_far)) {
+        if (named_bar_or(1 + ww, 64, mx > ref + 8.f || !ok)) {
           left = *reinterpret_cast<volatile int*>(&gave_up[ww]) != 0;
           if (left) break;
-          special = any_far;                            // the same in both warps: both have waited for v_full
           pair[h][r] = mx;
           named_bar(1 + ww, 64);
           mx = fmaxf(mx, pair[1 - h][r]);
@@ -411,33 +420,41 @@ pattn_bf16_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, const __
           for (int pt = 0; pt < kParts; ++pt) tmem_st8(tl + kTmP + 64u * pt + 32u * h + 8u * c, w[pt]);
         }
         lsum += sum;
-        if (special) {
-          // V elements that are not finite are zero in the tile: their p v is
-          // added here, to the rows that see them
+        // V elements that are not finite are zero in the tile: their p v is added
+        // here, to the rows that see them
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&v_full[st], (it / kStages) & 1));
+        const uint4 far = *reinterpret_cast<const uint4*>(&odd[it & 7][0]);
+        if (!ok) *reinterpret_cast<volatile int*>(&gave_up[ww]) = 1;
+        if (named_bar_or(1 + ww, 64, (far.x | far.y | far.z | far.w) != 0 || !ok)) {
+          left = *reinterpret_cast<volatile int*>(&gave_up[ww]) != 0;
+          if (left) break;
           const uint32_t mw[4] = {far.x, far.y, far.z, far.w};
+          tmem_wait_st();
+          tc_fence_before();
+          named_bar(1 + ww, 64);                        // both warps' p are in P
+          tc_fence_after();
 #pragma unroll 1
           for (int k = 0; k < kKeys; ++k) {
             if (!((mw[k >> 5] >> (k & 31)) & 1u)) continue;
-            const int t = t0 + k;
-            if ((k >> 6) == h) {
-              float y1 = 0.f;
+            uint32_t w[kParts];
 #pragma unroll
-              for (int e = 0; e < 64; ++e)
-                if (e == (k & 63)) y1 = x[e];
-              pair[0][r] = mine && t <= p && (t >= plow || t < sinks) ? y1 : -1.f;
-            }
-            named_bar(1 + ww, 64);
-            const float y1 = pair[0][r];
-            const uint16_t* vr = kv.pool + ((((size_t)page_at(kv, t >> 4) * kv.n_layers + layer) * 2 + 1) * kv.n_kv + kvh) * 2048 +
-                                 (t & 15) * 128 + 64 * h;
-            if (!(y1 < 0.f)) {
+            for (int pt = 0; pt < kParts; ++pt) w[pt] = tmem_ld1(tl + kTmP + 64u * pt + (k >> 1));
+            tmem_wait_ld();
+            float y1 = 0.f;
+#pragma unroll
+            for (int pt = 0; pt < kParts; ++pt)
+              y1 += __uint_as_float(k & 1 ? w[pt] & 0xFFFF0000u : w[pt] << 16);
+            const int t = t0 + k;
+            if (mine && t <= p && (t >= plow || t < sinks)) {
+              const uint16_t* vr = kv.pool + ((((size_t)page_at(kv, t >> 4) * kv.n_layers + layer) * 2 + 1) * kv.n_kv + kvh) * 2048 +
+                                   (t & 15) * 128 + 64 * h;
 #pragma unroll
               for (int c = 0; c < 64; ++c) {
                 const uint32_t w0 = vr[c];
                 if ((w0 & 0x7F80u) == 0x7F80u) acc[c] += y1 * __uint_as_float(w0 << 16);
               }
             }
-            named_bar(1 + ww, 64);
+            __syncwarp();
           }
         }
         if (pending && ok) drain();
