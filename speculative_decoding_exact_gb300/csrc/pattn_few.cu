@@ -26,6 +26,7 @@
 // Precision: as pattn.cu for the 4-bit cache (binary16, q and p in two parts,
 // row-wise powers of two).  bf16 pages are operands as they are, with q and p in
 // three bf16 parts (24 significant bits): no value is out of range.
+#include "attn_mma.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.cuh"
@@ -33,9 +34,29 @@
 
 namespace spec {
 
-constexpr int kFewWarps = 8;
+constexpr int kFewWarps = 12;
 constexpr int kOPitch = 132;               // floats between rows of a warp's O in shared memory
-constexpr size_t kFewSmem = sizeof(float) * kFewWarps * kFewRows * kOPitch;
+constexpr int kFewOBytes = 4 * kFewWarps * kFewRows * kOPitch;
+// A warp's ring of pages in shared memory.  Where a piece of 16 bytes lies keeps
+// the eight lanes of a load phase in different banks:
+//   4-bit: piece 16 c + t (chunk column c, key t) at 288 c + 16 t, then the scales
+//   bf16:  K row t at 288 t, V row t at 272 t + 16 (t / 8)
+template <bool k4>
+struct FewRing {
+  static constexpr int kK = k4 ? 4 * 288 + 128 : 16 * 288, kV = k4 ? kK : 16 * 272 + 16;
+  static constexpr int kSlots = k4 ? 5 : 2;
+  static constexpr int kWarp = kSlots * (kK + kV);
+  static constexpr size_t kSmem = kFewWarps * kWarp > kFewOBytes ? kFewWarps * kWarp : kFewOBytes;
+};
+// 16 bytes global -> shared, completion by group
+SPEC_DEV void copy16(uint8_t* dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+SPEC_DEV void copy_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int kPending>
+SPEC_DEV void copy_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(kPending) : "memory");
+}
 
 template <bool k4>
 SPEC_DEV void mma16816(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
@@ -47,11 +68,6 @@ SPEC_DEV void mma16816(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) 
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-}
-SPEC_DEV float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
 }
 // the operand part of a pair (x0 in the low half); x becomes what is left
 template <bool k4>
@@ -71,57 +87,6 @@ SPEC_DEV uint32_t take_part(float& x0, float& x1) {
   }
 }
 
-// A page as a lane loads it: K chunks of its key of both key tiles, V pieces of
-// its four keys
-template <bool k4>
-struct FewPage;
-template <>
-struct FewPage<true> {
-  uint4 k[2];
-  uint2 v[4];
-  uint32_t ks, vs;                         // word `lane` of the scales: groups 4 (lane % 2).. of key lane / 2
-};
-template <>
-struct FewPage<false> {
-  uint4 k[2][4], v[4][2];
-};
-SPEC_DEV uint2 ldg64_now(const void* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
-}
-SPEC_DEV uint4 ldg128_now(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
-// p: the K (V) page of the head
-SPEC_DEV void few_load_k(const uint8_t* p, int lane, FewPage<true>& r) {
-  const int n = lane >> 2, g = lane & 3;
-#pragma unroll
-  for (int nt = 0; nt < 2; ++nt) r.k[nt] = ldg128_now(p + kv4_chunk(4 * (n >> 1) + (n & 1) + 2 * nt, g));
-  r.ks = ldg_now((const void*)(p + kKv4Scales + 4 * lane));
-}
-SPEC_DEV void few_load_v(const uint8_t* p, int lane, FewPage<true>& r) {
-  const int n = lane >> 2, g = lane & 3;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) r.v[e] = ldg64_now(p + kv4_chunk(4 * g + e, n >> 1) + 8 * (n & 1));
-  r.vs = ldg_now((const void*)(p + kKv4Scales + 4 * lane));
-}
-SPEC_DEV void few_load_k(const uint8_t* p, int lane, FewPage<false>& r) {
-  const int n = lane >> 2, g = lane & 3;
-#pragma unroll
-  for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) r.k[nt][c] = ldg128_now(p + 256 * (4 * (n >> 1) + (n & 1) + 2 * nt) + 64 * g + 16 * c);
-}
-SPEC_DEV void few_load_v(const uint8_t* p, int lane, FewPage<false>& r) {
-  const int n = lane >> 2, g = lane & 3;
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) r.v[e][c] = ldg128_now(p + 256 * (4 * g + e) + 32 * n + 16 * c);
-}
 SPEC_DEV uint32_t word_of(const uint4& x, int i) { return i == 0 ? x.x : (i == 1 ? x.y : (i == 2 ? x.z : x.w)); }
 // f16 pair of byte b of w
 template <int B>
@@ -145,7 +110,9 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
   constexpr int kParts = k4 ? 2 : 3;                    // of q and p
   constexpr float kBias = k4 ? 7.f : 0.f;               // p = 2^(bias + s - max)
   constexpr int kPageBytes = k4 ? kKv4PageBytes : 4096;
-  extern __shared__ __align__(16) float o_sm[];         // [warp][row][kOPitch]
+  using Ring = FewRing<k4>;
+  extern __shared__ __align__(128) uint8_t sm[];
+  float* o_sm = reinterpret_cast<float*>(sm);           // [warp][row][kOPitch], where the rings were
   __shared__ uint4 qs[kParts][8][32];                   // A fragments
   __shared__ int qmax[kFewRows];
   __shared__ float2 ml_sm[kFewWarps][kFewRows];
@@ -155,23 +122,25 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
   const int slot = blockIdx.x, kvh = blockIdx.y, R = pl.M * pl.group;
   if (tid < kFewRows) qmax[tid] = 0;
   if (tid == 32) poison = 0;
+  uint8_t* ring = sm + warp * Ring::kWarp;
   pdl_trigger();
   pdl_wait();
   const int n_past = __ldcg(kv.seq_len) - pl.M;
-  // this thread's rows n and n + 8; in the first 8 warps Q elements 32 g + 4 warp
-  // .. (MMA `warp`'s)
+  // this thread's rows n and n + 8; in the first 8 warps the Q elements of MMA
+  // `warp` (bf16: the 16-byte pieces of a K row in an order that depends on g)
+  const int q_at = k4 ? 32 * g + 4 * warp : 32 * g + 8 * ((warp >> 1) ^ (g >> 1)) + 4 * (warp & 1);
   float4 qv[2];
   int pos[2], plow[2], row_i[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int r = n + 8 * h;
-    row_i[h] = r < R ? r / pl.group : -1;
+    row_i[h] = r < R ? div24(r, pl.group) : -1;
     pos[h] = n_past + row_i[h];
     plow[h] = window_low(pl, pos[h]);
     qv[h] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < R && warp < 8)
       qv[h] = *reinterpret_cast<const float4*>(
-          q + ((size_t)row_i[h] * pl.nq + kvh * pl.group + r - row_i[h] * pl.group) * 128 + 32 * g + 4 * warp);
+          q + ((size_t)row_i[h] * pl.nq + kvh * pl.group + r - row_i[h] * pl.group) * 128 + q_at);
   }
   const int passes = span_count(pl, n_past);
   TileList tl0 = tiles_of(span_of(pl, n_past, 0), slot), tl1;
@@ -179,6 +148,69 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
   if (tl0.n + tl1.n == 0) return;
   const int b_last = n_past + pl.M - 1;                 // the block's last position
   const int low0 = window_low(pl, n_past), low1 = window_low(pl, b_last), sinks = pl.window > 0 ? pl.sinks : 0;
+
+  const uint32_t stride = (uint32_t)(kv.n_layers * 2 * kv.n_kv * kPageBytes);
+  const uint8_t* kbase = reinterpret_cast<const uint8_t*>(kv.pool) + (size_t)(layer * 2 * kv.n_kv + kvh) * kPageBytes;
+  const uint8_t* vbase = kbase + (size_t)kv.n_kv * kPageBytes;
+
+  // This warp's pages: those of the chunk whose number is `warp` mod 12.
+  TileList tl;
+  int f0, f1, c0, pages;
+  auto page_no = [&](int j) {
+    return j < c0 ? tl.a0 * kPagesPerTile + f0 + kFewWarps * j : tl.a1 * kPagesPerTile + f1 + kFewWarps * (j - c0);
+  };
+  auto id_of = [&](int j) { return j < pages ? page_at(kv, page_no(j)) : -1; };
+  // Copies page j into slot b if it is mapped and some row of the block sees a key
+  // of it; whether it was.
+  auto fetch = [&](int j, int id, int b) {
+    if (j >= pages || !page_ok(kv, id)) return false;
+    const int k0 = 16 * page_no(j);
+    if (k0 > b_last || (k0 + 15 < low0 && k0 >= sinks)) return false;
+    uint8_t* dst = ring + b * (Ring::kK + Ring::kV);
+    const uint8_t* kp = kbase + (uint64_t)(uint32_t)id * stride;
+    const uint8_t* vp = vbase + (uint64_t)(uint32_t)id * stride;
+    if constexpr (k4) {
+      const int at = 288 * (lane >> 4) + 16 * (lane & 15);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        copy16(dst + at + 576 * i, kp + 16 * lane + 512 * i);
+        copy16(dst + Ring::kK + at + 576 * i, vp + 16 * lane + 512 * i);
+      }
+      if (lane < 16)                                    // the scales of K, of V
+        copy16(dst + (lane < 8 ? 0 : Ring::kK) + 4 * 288 + 16 * (lane & 7), (lane < 8 ? kp : vp) + kKv4Scales + 16 * (lane & 7));
+    } else {
+      const int t0 = lane >> 4, at = 16 * (lane & 15);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {                     // rows 2 i + t0
+        copy16(dst + 288 * (2 * i + t0) + at, kp + 16 * lane + 512 * i);
+        copy16(dst + Ring::kK + 272 * (2 * i + t0) + 16 * (i >> 2) + at, vp + 16 * lane + 512 * i);
+      }
+    }
+    return true;
+  };
+  uint32_t have = 0;                                    // bit b: slot b holds a page, or will
+  int id_next = -1, id_after = -1;                      // ids of the two pages behind those of the ring
+  auto start = [&](int pass) {
+    tl = pass == 0 ? tl0 : tl1;
+    const int n0 = tl.n0 * kPagesPerTile, n1 = (tl.n - tl.n0) * kPagesPerTile;
+    auto first_of = [&](int from) { return (int)((unsigned)(warp + kFewWarps - (unsigned)from % kFewWarps) % kFewWarps); };
+    f0 = first_of(tl.a0 * kPagesPerTile);
+    f1 = first_of(tl.a1 * kPagesPerTile);
+    c0 = n0 > f0 ? (n0 - f0 + kFewWarps - 1) / kFewWarps : 0;
+    pages = c0 + (n1 > f1 ? (n1 - f1 + kFewWarps - 1) / kFewWarps : 0);
+    int id[Ring::kSlots];
+#pragma unroll
+    for (int b = 0; b < Ring::kSlots; ++b) id[b] = id_of(b);
+    id_next = id_of(Ring::kSlots);
+    id_after = id_of(Ring::kSlots + 1);
+    have = 0;
+#pragma unroll
+    for (int b = 0; b < Ring::kSlots; ++b) {
+      if (fetch(b, id[b], b)) have |= 1u << b;
+      copy_commit();
+    }
+  };
+  start(0);
 
   // log2(e) / sqrt(d), for the 4-bit cache times the row's power of two
   float unit[2];
@@ -213,14 +245,9 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
   }
   __syncthreads();
 
-  const uint32_t stride = (uint32_t)(kv.n_layers * 2 * kv.n_kv * kPageBytes);
-  const uint8_t* kbase = reinterpret_cast<const uint8_t*>(kv.pool) + (size_t)(layer * 2 * kv.n_kv + kvh) * kPageBytes;
-  const uint8_t* vbase = kbase + (size_t)kv.n_kv * kPageBytes;
-
 #pragma unroll 1
   for (int pass = 0; pass < passes; ++pass) {
     const Span sp = span_of(pl, n_past, pass);
-    const TileList tl = pass == 0 ? tl0 : tl1;
     bool mine[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) mine[h] = row_i[h] >= sp.i0 && row_i[h] < sp.i1;
@@ -229,74 +256,56 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
     for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
     float ref[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
 
-    // This warp's pages: those of the chunk whose number is `warp` mod 12.  K of
-    // the next one is loaded once K of this one has been used, V likewise; page
-    // ids are fetched a step earlier.
-    const int n0 = tl.n0 * kPagesPerTile, n1 = (tl.n - tl.n0) * kPagesPerTile;
-    auto first_of = [&](int from) { return (int)((unsigned)(warp + kFewWarps - (unsigned)from % kFewWarps) % kFewWarps); };
-    const int f0 = first_of(tl.a0 * kPagesPerTile), f1 = first_of(tl.a1 * kPagesPerTile);
-    const int c0 = n0 > f0 ? (n0 - f0 + kFewWarps - 1) / kFewWarps : 0;
-    const int pages = c0 + (n1 > f1 ? (n1 - f1 + kFewWarps - 1) / kFewWarps : 0);
-    auto page_no = [&](int j) {
-      return j < c0 ? tl.a0 * kPagesPerTile + f0 + kFewWarps * j : tl.a1 * kPagesPerTile + f1 + kFewWarps * (j - c0);
-    };
-    auto id_of = [&](int j) { return j < pages ? page_at(kv, page_no(j)) : -1; };
-    // a mapped page with a key that some row of the block sees
-    auto wanted = [&](int j, int page) {
-      if (j >= pages || !page_ok(kv, page)) return false;
-      const int k0 = 16 * page_no(j);
-      return k0 <= b_last && (k0 + 15 >= low0 || k0 < sinks);
-    };
-    FewPage<k4> cur;
-    int id0 = id_of(0), id1 = id_of(1);
-    bool want = wanted(0, id0);
-    if (want) {
-      few_load_k(kbase + (uint64_t)(uint32_t)id0 * stride, lane, cur);
-      few_load_v(vbase + (uint64_t)(uint32_t)id0 * stride, lane, cur);
-    }
+    int b = 0;                                          // slot of page j
 #pragma unroll 1
     for (int j = 0; j < pages; ++j) {
-      const int id2 = id_of(j + 2);
-      const bool want1 = wanted(j + 1, id1);
-      const uint8_t* knext = kbase + (uint64_t)(uint32_t)id1 * stride;
-      const uint8_t* vnext = vbase + (uint64_t)(uint32_t)id1 * stride;
-      if (want) {
+      copy_wait<Ring::kSlots - 1>();
+      __syncwarp();
+      if ((have >> b) & 1u) {
+        const uint8_t* kp = ring + b * (Ring::kK + Ring::kV);
+        const uint8_t* vp = kp + Ring::kK;
         const int k0 = 16 * page_no(j);
         // ------------------------------------------------ S = Q . K^T
         float s[2][2][4] = {};                          // [key tile][high part, low parts]
-        uint32_t ksc[2][2];
+        uint32_t ksc[2][2], ks_word = 0, vs_word = 0;   // word `lane` of the scales: groups 4 (lane % 2).. of key lane / 2
+        uint4 kc[2];
         if constexpr (k4) {
+          ks_word = *reinterpret_cast<const uint32_t*>(kp + 4 * 288 + 4 * lane);
+          vs_word = *reinterpret_cast<const uint32_t*>(vp + 4 * 288 + 4 * lane);
           // scales 2 g and 2 g + 1 of this lane's keys
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt) {
             const uint32_t w =
-                __shfl_sync(0xffffffffu, cur.ks, 2 * (4 * (n >> 1) + (n & 1) + 2 * nt) + (g >> 1)) >> (16 * (g & 1));
+                __shfl_sync(0xffffffffu, ks_word, 2 * (4 * (n >> 1) + (n & 1) + 2 * nt) + (g >> 1)) >> (16 * (g & 1));
             ksc[nt][0] = scale_pair(w & 0xFFu);
             ksc[nt][1] = scale_pair((w >> 8) & 0xFFu);
           }
         }
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
-          uint32_t b[2][2];
+          uint32_t kb[2][2];
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt) {
+            const int t = 4 * (n >> 1) + (n & 1) + 2 * nt;      // this lane's key
             if constexpr (k4) {
-              const uint32_t w = word_of(cur.k[nt], ks >> 1), s2 = ksc[nt][ks >> 2];
-              b[nt][0] = hmul2_u32(e2m1_pick(w, 2 * (ks & 1)), s2);
-              b[nt][1] = hmul2_u32(e2m1_pick(w, 2 * (ks & 1) + 1), s2);
+              if (ks == 0) kc[nt] = *reinterpret_cast<const uint4*>(kp + 288 * g + 16 * t);
+              const uint32_t w = word_of(kc[nt], ks >> 1), s2 = ksc[nt][ks >> 2];
+              kb[nt][0] = hmul2_u32(e2m1_pick(w, 2 * (ks & 1)), s2);
+              kb[nt][1] = hmul2_u32(e2m1_pick(w, 2 * (ks & 1) + 1), s2);
             } else {
-              b[nt][0] = word_of(cur.k[nt][ks >> 1], 2 * (ks & 1));
-              b[nt][1] = word_of(cur.k[nt][ks >> 1], 2 * (ks & 1) + 1);
+              if ((ks & 1) == 0)
+                kc[nt] = *reinterpret_cast<const uint4*>(kp + 288 * t + 64 * g + 16 * ((ks >> 1) ^ (g >> 1)));
+              kb[nt][0] = word_of(kc[nt], 2 * (ks & 1));
+              kb[nt][1] = word_of(kc[nt], 2 * (ks & 1) + 1);
             }
           }
 #pragma unroll
           for (int pt = kParts - 1; pt >= 0; --pt) {
             const uint4 a = qs[pt][ks][lane];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) mma16816<k4>(s[nt][pt > 0], a, b[nt][0], b[nt][1]);
+            for (int nt = 0; nt < 2; ++nt) mma16816<k4>(s[nt][pt > 0], a, kb[nt][0], kb[nt][1]);
           }
         }
-        if (want1) few_load_k(knext, lane, cur);
         // x[h][e]: row n + 8 h, key k0 + 4 g + e
         float x[2][4];
 #pragma unroll
@@ -304,6 +313,18 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             x[h][e] = (s[e >> 1][0][2 * h + (e & 1)] + s[e >> 1][1][2 * h + (e & 1)]) * unit[h];
+        uint2 v4[4];                                    // V pieces of this lane's four keys
+        uint4 v16[4][2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = 4 * g + e;
+          if constexpr (k4)
+            v4[e] = *reinterpret_cast<const uint2*>(vp + 288 * (n >> 1) + 16 * t + 8 * (n & 1));
+          else
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              v16[e][c] = *reinterpret_cast<const uint4*>(vp + 272 * t + 16 * (g >> 1) + 32 * n + 16 * c);
+        }
         // some row of the block does not see some key of the page
         const bool masked = k0 + 15 > n_past || (k0 < low1 && k0 + 16 > sinks) || passes > 1;
         if (masked) {
@@ -326,7 +347,7 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
               bool bad = false;
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                uint32_t* w = reinterpret_cast<uint32_t*>(&cur.v[e][c]);
+                uint32_t* w = reinterpret_cast<uint32_t*>(&v16[e][c]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                   const bool lo = (w[i] & 0x7F80u) == 0x7F80u, hi = (w[i] & 0x7F800000u) == 0x7F800000u;
@@ -355,7 +376,7 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
             a[h] = 1.f;
             if (mx[h] > ref[h] + 8.f) {
-              if (ref[h] != -INFINITY) a[h] = ex2(ref[h] - mx[h]);
+              if (ref[h] != -INFINITY) a[h] = exp2_approx(ref[h] - mx[h]);
               ref[h] = mx[h];
             }
             lsum[h] *= a[h];
@@ -374,7 +395,7 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
           const float base = kBias - (ref[h] == -INFINITY ? 0.f : ref[h]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x[h][e] = ex2(x[h][e] + base);
+            x[h][e] = exp2_approx(x[h][e] + base);
             lsum[h] += x[h][e];
           }
         }
@@ -390,42 +411,44 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
         if constexpr (k4) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)                   // scale byte n of keys 4 g + e
-            s2[e] = scale_pair((__shfl_sync(0xffffffffu, cur.vs, 2 * (4 * g + e) + (n >> 2)) >> (8 * (n & 3))) & 0xFFu);
+            s2[e] = scale_pair((__shfl_sync(0xffffffffu, vs_word, 2 * (4 * g + e) + (n >> 2)) >> (8 * (n & 3))) & 0xFFu);
         }
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {                // d's 16 n + 2i .. 2i + 3: four independent sums
-          uint32_t b[4][2];
+          uint32_t vb[4][2];
 #pragma unroll
           for (int ii = 0; ii < 2; ++ii) {
             uint32_t v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               if constexpr (k4)
-                v[e] = hmul2_u32(e2m1_pick(i < 4 ? cur.v[e].x : cur.v[e].y, (i & 3) + ii), s2[e]);
+                v[e] = hmul2_u32(e2m1_pick(i < 4 ? v4[e].x : v4[e].y, (i & 3) + ii), s2[e]);
               else
-                v[e] = word_of(cur.v[e][i >> 2], (i & 3) + ii);
+                v[e] = word_of(v16[e][i >> 2], (i & 3) + ii);
             }
 #pragma unroll
             for (int hl = 0; hl < 2; ++hl) {
               const uint32_t sel = hl ? 0x7632u : 0x5410u;
-              b[2 * ii + hl][0] = __byte_perm(v[0], v[1], sel);
-              b[2 * ii + hl][1] = __byte_perm(v[2], v[3], sel);
+              vb[2 * ii + hl][0] = __byte_perm(v[0], v[1], sel);
+              vb[2 * ii + hl][1] = __byte_perm(v[2], v[3], sel);
             }
           }
 #pragma unroll
           for (int pt = kParts - 1; pt >= 0; --pt)
 #pragma unroll
-            for (int jj = 0; jj < 4; ++jj) mma16816<k4>(o[2 * i + jj], pa[pt], b[jj][0], b[jj][1]);
+            for (int jj = 0; jj < 4; ++jj) mma16816<k4>(o[2 * i + jj], pa[pt], vb[jj][0], vb[jj][1]);
         }
       }
-      if (want1) {
-        if (!want) few_load_k(knext, lane, cur);
-        few_load_v(vnext, lane, cur);
-      }
-      want = want1;
-      id0 = id1;
-      id1 = id2;
+      // the slot takes page j + kSlots
+      __syncwarp();
+      have &= ~(1u << b);
+      if (fetch(j + Ring::kSlots, id_next, b)) have |= 1u << b;
+      copy_commit();
+      id_next = id_after;
+      id_after = id_of(j + Ring::kSlots + 2);
+      b = b + 1 == Ring::kSlots ? 0 : b + 1;
     }
+    __syncthreads();                                    // the rings are free
     // ---- join the warps, in order.  Row n + 8 h, d's 32 g + 16 e + (MMA index).
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -464,7 +487,7 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
       for (int w = 0; w < kFewWarps; ++w) {
         const float2 v = ml_sm[w][r];
         if (v.y == 0.f) continue;                       // the row sees no key of this warp
-        const float a = ex2(v.x - m);
+        const float a = exp2_approx(v.x - m);
         const float4 z = *reinterpret_cast<const float4*>(o_sm + ((size_t)w * kFewRows + r) * kOPitch + 4 * lane);
         L += a * v.y;
         y.x += a * z.x;
@@ -488,7 +511,10 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
       reinterpret_cast<float4*>(part_o)[(((size_t)slot * pl.nkv + kvh) * 32 + lane) * R + r] = y;
       if (lane == 0) part_ml[at] = make_float2(m, L);
     }
-    __syncthreads();                                    // the shared memory is free for the next pass
+    if (pass + 1 < passes) {
+      __syncthreads();                                  // the shared memory is free for the next pass
+      start(1);
+    }
   }
 }
 
@@ -503,11 +529,11 @@ static cudaError_t launch_few(const PattnPlan& pl, const KvView& kv, int layer, 
   if (e != cudaSuccess) return e;
   const bool known = dev >= 0 && dev < kMaxDevices;
   if (!known || !have[dev]) {
-    e = cudaFuncSetAttribute(pattn_few_kernel<k4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSmem);
+    e = cudaFuncSetAttribute(pattn_few_kernel<k4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FewRing<k4>::kSmem);
     if (e != cudaSuccess) return e;
     if (known) have[dev] = true;
   }
-  pattn_few_kernel<k4><<<dim3(pl.slots, pl.nkv), 32 * kFewWarps, kFewSmem, st>>>(q, pl, kv, layer, part_o, part_ml);
+  pattn_few_kernel<k4><<<dim3(pl.slots, pl.nkv), 32 * kFewWarps, FewRing<k4>::kSmem, st>>>(q, pl, kv, layer, part_o, part_ml);
   return cudaGetLastError();
 }
 
