@@ -45,6 +45,8 @@ constexpr int kHalf = kKeys * 128;                  // one d half of a K or V ti
 constexpr int kStageBytes = 4 * kHalf;              // K then V, 64 KB
 
 constexpr int kStages = 3;                          // [d half][key][128 B], 128-byte swizzle; K, then V
+constexpr int kUnpackWarps = 6;
+constexpr int kItemsPerTile = kPagesPerTile / 2;    // what an unpacking warp takes at once: two pages, 32 keys
 constexpr size_t kPattnSmem = 1024 + (size_t)kStages * kStageBytes;
 // TMEM columns: two score buffers, each overwritten in place by its P parts
 // (16 columns of high and 16 of low parts per 32 keys); O; Q (64 columns of high
@@ -54,22 +56,20 @@ constexpr int kTmAll = 512;
 
 // warps: 0-7 softmax, two threads per row (warp w: rows 32 (w % 4).., keys and
 // d's 64 (w / 4)..), 8 issues the QK MMAs, 9 the PV MMAs, 10-15 unpack pages of K
-// and V in turn.  The launch gives every thread
-// 128 registers, 65,536 in all; the softmax threads take 176 (bf16: 160) of them
-// and the others 80 (96).
-constexpr int kSoftWarps = 8, kWQk = 8, kWPv = 9, kWLoad = 10, kUnpackWarps = 6;
+// and V in turn.  The launch gives every thread 128 registers, 65,536 in all; the
+// softmax threads take 184 of them and the others 72.
+constexpr int kSoftWarps = 8, kWQk = 8, kWPv = 9, kWLoad = 10;
 constexpr int kPattnThreads = 512;
 
 using f2 = unsigned long long;                      // two floats for the packed fp32 instructions
 // binary16 parts of a pair: hi nearest, lo what is left (the first in the low half)
 SPEC_DEV void split_pair(f2 x, uint32_t& hi, uint32_t& lo) {
-  float x0, x1, r0, r1;
+  float x0, x1;
   f2unpack(x, x0, x1);
   const __half2 h = __floats2half2_rn(x0, x1);
-  const float2 f = __half22float2(h);
-  f2unpack(f2sub(x, f2pack(f.x, f.y)), r0, r1);
-  const __half2 l = __floats2half2_rn(r0, r1);
   hi = *reinterpret_cast<const uint32_t*>(&h);
+  minus_f16x2(x0, x1, hi);
+  const __half2 l = __floats2half2_rn(x0, x1);
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 // 32 consecutive TMEM columns of this warp's 32 lanes, as pairs (to be waited for)
@@ -87,69 +87,45 @@ SPEC_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
 }
 
-// One page of a tile as an unpacking warp holds it.
-// 4-bit: lane = key % 16 + 16 * d half; 64 codes and 4 scale bytes of K or V.
+// One key of K or V: codes and scale bytes
 struct Raw4 {
-  uint4 c[2];
-  uint32_t s;
+  uint4 c[4];
+  uint2 s;
 };
-// base: this lane's first chunk of page 0 of the layer and head; stride: bytes
-// of a page of the pool
-SPEC_DEV void load_page(const uint8_t* base, uint32_t stride, int page, bool there, int scales, Raw4& r) {
+// p: the page's chunk 0 of the key; scales: from there to its scale bytes
+SPEC_DEV void load_key(const uint8_t* p, int scales, bool there, Raw4& r) {
   if (!there) {                                          // unmapped: zeros (its keys are masked)
-    r.c[0] = r.c[1] = make_uint4(0, 0, 0, 0);
-    r.s = 0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) r.c[c] = make_uint4(0, 0, 0, 0);
+    r.s = make_uint2(0, 0);
     return;
   }
-  const uint8_t* p = base + (uint64_t)(uint32_t)page * stride;
-  r.c[0] = ldg_now(reinterpret_cast<const uint4*>(p));
-  r.c[1] = ldg_now(reinterpret_cast<const uint4*>(p + 256));
-  r.s = ldg_now((const void*)(p + scales));
-}
-// the 64 values of one key and d half as binary16 into a tile's row (128
-// bytes, 16-byte chunk j at j ^ (row % 8)); the eight lanes of a store phase
-// hold different rows % 8, so no two meet in a bank
-SPEC_DEV void unpack_row(const uint4 (&codes)[2], uint32_t scales, uint8_t* row, int r7) {
-  const uint32_t sc = __vminu4(scales, 0xE2E2E2E2u);
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const uint32_t w[4] = {codes[c].x, codes[c].y, codes[c].z, codes[c].w};
+  for (int c = 0; c < 4; ++c) r.c[c] = ldg_now(reinterpret_cast<const uint4*>(p + 256 * c));
+  r.s = ldg_now(reinterpret_cast<const uint2*>(p + scales));
+}
+// the 128 values of a key as binary16 into its row of the tile's d halves (128
+// bytes each, 16-byte chunk j at j ^ (row % 8)); the eight lanes of a store phase
+// hold different rows % 8, so no two meet in a bank
+SPEC_DEV void unpack_key(const Raw4& r, uint8_t* row, int r7) {
+  const uint32_t sc[2] = {__vminu4(r.s.x, 0xE2E2E2E2u), __vminu4(r.s.y, 0xE2E2E2E2u)};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t w[4] = {r.c[c].x, r.c[c].y, r.c[c].z, r.c[c].w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t s2 = ((sc >> (8 * (2 * c + (j >> 1)))) & 0xFFu) * 0x00800080u;   // (byte << 7) in both halves
+      const uint32_t s2 = ((sc[c >> 1] >> (8 * (2 * (c & 1) + (j >> 1)))) & 0xFFu) * 0x00800080u;   // (byte << 7) in both halves
       uint32_t f[4];
       e2m1_word(w[j], f);
-      const int ch = 4 * c + j;
-      *reinterpret_cast<uint4*>(row + ((ch ^ r7) << 4)) =
+      *reinterpret_cast<uint4*>(row + (c >> 1) * kHalf + (((4 * (c & 1) + j) ^ r7) << 4)) =
           make_uint4(hmul2_u32(f[0], s2), hmul2_u32(f[1], s2), hmul2_u32(f[2], s2), hmul2_u32(f[3], s2));
     }
   }
 }
-// bf16: load j of K or V is the 16-byte chunk lane % 16 of row 2j + lane / 16
-struct Raw16 {
-  uint4 x[8];
-};
-SPEC_DEV void load_rows(const uint4* base, uint32_t stride, int page, bool there, Raw16& r) {
-  if (!there) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) r.x[j] = make_uint4(0, 0, 0, 0);
-    return;
-  }
-  const uint4* p = base + (uint64_t)(uint32_t)page * stride;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) r.x[j] = ldg_now(p + 32 * j);
-}
-// bf16 pair as binary16; |x| >= 2^16, infinities and NaN are the caller's business
-SPEC_DEV uint32_t bf16x2_to_f16x2(uint32_t w) {
-  const __half2 h = __floats2half2_rn(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-constexpr uint32_t kBf16Limit = 0x4780u;            // bf16 bits of 2^16: binary16 holds every bf16 value below
 
 // ---------------------------------------------------------------------------
 // partials: grid (slot, KV head, row tile)
 // ---------------------------------------------------------------------------
-template <bool k4>
 __global__ void __launch_bounds__(kPattnThreads, 1)
 pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, float* __restrict__ part_o,
              float2* __restrict__ part_ml, int32_t* status) {
@@ -159,10 +135,8 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
   __shared__ __align__(8) uint64_t q_full, k_full[kStages], v_full[kStages], k_free[kStages], v_free[kStages],
       s_full[2], p_full[2], pv_done[2];
   __shared__ float pair[2][128];                        // what the two threads of a row exchange
-  // per tile (a ring of 8: a tile's entries are rewritten eight tiles later,
-  // when its softmax has long been passed): mapped pages, and for bf16 the keys
-  // whose K or V has an element out of range
-  __shared__ __align__(16) uint16_t odd[2][8][kPagesPerTile];
+  // mapped pages per tile (a ring of 8: a tile's entries are rewritten eight tiles
+  // later, when its softmax has long been passed)
   __shared__ __align__(8) uint8_t mapped[8][kPagesPerTile];
   __shared__ int gave_up[4];                            // a wait of this pair of softmax warps ran out
 
@@ -174,8 +148,8 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
   if (tid == 32 * kWPv) {
     mbar_init(&q_full, 2 * row_warps);
     for (int b = 0; b < kStages; ++b) {
-      mbar_init(&k_full[b], kPagesPerTile);
-      mbar_init(&v_full[b], kPagesPerTile);
+      mbar_init(&k_full[b], kItemsPerTile);
+      mbar_init(&v_full[b], kItemsPerTile);
       mbar_init(&k_free[b], 1);
       mbar_init(&v_free[b], 1);
     }
@@ -190,6 +164,19 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
   pdl_trigger();
   pdl_wait();
   const int n_past = __ldcg(kv.seq_len) - pl.M;
+  // the rows of Q, whole rows by a warp, into the last stage (which tile 2 is the
+  // first to use), 16-byte chunk j at j ^ (row % 8)
+  uint8_t* q_rows = sm + (kStages - 1) * kStageBytes;
+#pragma unroll
+  for (int j = 0; j < 128 / (kPattnThreads / 32); ++j) {
+    const int r = warp + (kPattnThreads / 32) * j, fr = r0 + r;
+    if (r < nr) {
+      const int i = div24(fr, pl.group);
+      copy16(q_rows + 512 * r + ((lane ^ (r & 7)) << 4),
+             reinterpret_cast<const uint8_t*>(q + ((size_t)i * pl.nq + kvh * pl.group + fr - i * pl.group) * 128) + 16 * lane);
+    }
+  }
+  copy_commit();
   const int passes = span_count(pl, n_past);
   TileList tl0 = tiles_of(span_of(pl, n_past, 0), slot), tl1;
   if (passes == 2) tl1 = tiles_of(span_of(pl, n_past, 1), slot);
@@ -197,182 +184,72 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
   auto tile_at = [&](int it) { return it < tl0.n ? tl0.at(it) : tl1.at(it - tl0.n); };
   const int b_last = n_past + pl.M - 1;                 // the block's last position
   const int low0 = window_low(pl, n_past), low1 = window_low(pl, b_last), sinks = pl.window > 0 ? pl.sinks : 0;
+  copy_wait<0>();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   // ---------------------------------------------------------------- unpack
-  // Item g is page g % 8 of tile g / 8; warp id of `count` takes every count-th.
-  // A step waits, unpacks and signals for two pages at once, the V of one item
-  // and the K of the next (whose stage is freed earlier): a lone warp issues an
-  // instruction every four or five cycles, and two independent streams fill
-  // some of the gaps.  The registers hold the next step's pages.
-  auto unpack = [&](int id, int count) {
-    const int items = total * kPagesPerTile;
-    auto page_of = [&](int g) { return g < items ? page_at(kv, tile_at(g >> 3) * kPagesPerTile + (g & 7)) : -1; };
-    // this item's stage, once its former K (V) has been read
-    auto free_k = [&](int it) {
-      return it < kStages || __all_sync(0xffffffffu, mbar_wait(&k_free[it % kStages], ((it / kStages) - 1) & 1));
+  // Item g is pages 2 (g % 4) and the next of tile g / 4, a key per lane; warp id
+  // takes every kUnpackWarps-th.  A step waits, unpacks and signals for K of one
+  // item and V of the item before (whose stage is freed later).  The registers hold
+  // the next step's keys.  (With items of one page, where the bookkeeping weighs
+  // more than the unpacking, 208 rows over 32k keys took 43 instead of 39 us;
+  // filling slots in shared memory by cp.async two steps ahead was no faster.)
+  auto unpack = [&](int id) {
+    const int items = total * kItemsPerTile;
+    auto page_of = [&](int g) {
+      return g < items ? page_at(kv, tile_at(g / kItemsPerTile) * kPagesPerTile + 2 * (g % kItemsPerTile) + (lane >> 4)) : -1;
     };
-    auto free_v = [&](int it) {
-      return it < kStages || __all_sync(0xffffffffu, mbar_wait(&v_free[it % kStages], ((it / kStages) - 1) & 1));
+    const uint32_t stride = (uint32_t)(kv.n_layers * 2 * kv.n_kv) * kKv4PageBytes;
+    const int t = lane & 15, scales = kKv4Scales + 8 * t - 16 * t;
+    const uint8_t* kb = reinterpret_cast<const uint8_t*>(kv.pool) + (size_t)(layer * 2 * kv.n_kv + kvh) * kKv4PageBytes + 16 * t;
+    const uint8_t* vb = kb + kv.n_kv * kKv4PageBytes;
+    auto load = [&](const uint8_t* base, int page, Raw4& r) {
+      load_key(base + (uint64_t)(uint32_t)page * stride, scales, page_ok(kv, page), r);
     };
+    // the pages of this V, of this step's K, and of the K after that
+    int page = page_of(id), next = page_of(id + kUnpackWarps), after = page_of(id + 2 * kUnpackWarps);
     bool ok = true;
-    if constexpr (k4) {
-      const int t = lane & 15, half = lane >> 4;
-      uint8_t* row0 = sm + half * kHalf + t * 128;
-      const uint32_t stride = (uint32_t)(kv.n_layers * 2 * kv.n_kv) * kKv4PageBytes;
-      const uint8_t* kb = reinterpret_cast<const uint8_t*>(kv.pool) +
-                          (size_t)(layer * 2 * kv.n_kv + kvh) * kKv4PageBytes + kv4_chunk(t, 2 * half);
-      const uint8_t* vb = kb + kv.n_kv * kKv4PageBytes;
-      const int scales = kKv4Scales + 8 * t + 4 * half - kv4_chunk(t, 2 * half);
-      // the pages of this V, of this step's K, and of the K after that
-      int page = page_of(id), next = page_of(id + count), after = page_of(id + 2 * count);
-      Raw4 k, v;
-      load_page(kb, stride, page, page_ok(kv, page), scales, k);
-      load_page(vb, stride, page, page_ok(kv, page), scales, v);
-      for (int g = id - count; ok && g < items; g += count) {
-        const int gk = g + count, itk = gk >> 3, stk = itk % kStages, it = g >> 3, st = it % kStages;
-        const bool has_k = gk < items, has_v = g >= 0;
-        if (has_k) ok = free_k(itk);
-        if (has_v) ok = ok && free_v(it);
-        if (!ok) break;
-        if (has_k) unpack_row(k.c, k.s, row0 + stk * kStageBytes + (gk & 7) * 2048, t & 7);
-        if (has_v) unpack_row(v.c, v.s, row0 + st * kStageBytes + 2 * kHalf + (g & 7) * 2048, t & 7);
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-          if (has_k) {
-            mapped[itk & 7][gk & 7] = page_ok(kv, has_v ? next : page);
-            mbar_arrive(&k_full[stk]);
-          }
-          if (has_v) mbar_arrive(&v_full[st]);
-        }
-        // K of the step after; V of the item whose K was just unpacked
-        const int nk = has_v ? after : next;
-        load_page(kb, stride, nk, page_ok(kv, nk), scales, k);
-        if (has_v) {
-          load_page(vb, stride, next, page_ok(kv, next), scales, v);
-          page = next;
-          next = after;
-          after = page_of(gk + 2 * count);
-        }
+    Raw4 k, v;
+    load(kb, page, k);
+    load(vb, page, v);
+    for (int g = id - kUnpackWarps; ok && g < items; g += kUnpackWarps) {
+      const int gk = g + kUnpackWarps, itk = gk / kItemsPerTile, stk = itk % kStages, it = g / kItemsPerTile, st = it % kStages;
+      const bool has_k = gk < items, has_v = g >= 0;
+      // the stage, once its former K (V) has been read
+      if (has_k && itk >= kStages) ok = mbar_wait(&k_free[stk], ((itk / kStages) - 1) & 1);
+      if (has_k && itk == kStages - 1) ok = mbar_wait(&q_full, 0);      // Q's rows lay in this stage
+      if (has_v && it >= kStages) ok = ok && mbar_wait(&v_free[st], ((it / kStages) - 1) & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (has_k) unpack_key(k, sm + stk * kStageBytes + (gk % kItemsPerTile) * 4096 + lane * 128, lane & 7);
+      if (has_v) unpack_key(v, sm + st * kStageBytes + 2 * kHalf + (g % kItemsPerTile) * 4096 + lane * 128, lane & 7);
+      fence_proxy_async();
+      if (has_k && t == 0) mapped[itk & 7][2 * (gk % kItemsPerTile) + (lane >> 4)] = page_ok(kv, has_v ? next : page);
+      __syncwarp();
+      if (lane == 0) {
+        if (has_k) mbar_arrive(&k_full[stk]);
+        if (has_v) mbar_arrive(&v_full[st]);
       }
-    } else {
-      // (16-byte units; a page of one head is 256 of them)
-      const uint32_t stride = (uint32_t)(kv.n_layers * 2 * kv.n_kv) * 256u;
-      const uint4* kb = reinterpret_cast<const uint4*>(kv.pool) + (size_t)(layer * 2 * kv.n_kv + kvh) * 256 + lane;
-      const uint4* vb = kb + kv.n_kv * 256;
-      int page = page_of(id), next = page_of(id + count), after = page_of(id + 2 * count);
-      Raw16 k, v;
-      load_rows(kb, stride, page, page_ok(kv, page), k);
-      load_rows(vb, stride, page, page_ok(kv, page), v);
-      // chunk j of this lane: row 2j + lane / 16, 16-byte chunk lane % 16
-      const int ch = lane & 15, rh = lane >> 4;
-      uint8_t* dst0 = sm + (ch >> 3) * kHalf + rh * 128;
-      auto put = [&](const Raw16& r, uint8_t* dst) {
-        __half2 top = __floats2half2_rn(0.f, 0.f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint4 y = make_uint4(bf16x2_to_f16x2(r.x[j].x), bf16x2_to_f16x2(r.x[j].y), bf16x2_to_f16x2(r.x[j].z),
-                               bf16x2_to_f16x2(r.x[j].w));
-          const __half2* yh = reinterpret_cast<const __half2*>(&y);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = __hmax2_nan(top, __habs2(yh[e]));
-          *reinterpret_cast<uint4*>(dst + j * 256 + (((ch & 7) ^ ((2 * j + rh) & 7)) << 4)) = y;
-        }
-        const uint32_t m = *reinterpret_cast<const uint32_t*>(&top);
-        return (m & 0x7C00u) == 0x7C00u || (m & 0x7C000000u) == 0x7C000000u;     // past binary16, or not finite
-      };
-      // the same with every row looked at: elements past binary16 are zeroed
-      // and their rows returned; V rows that no row of the block sees are
-      // zeroed (stale bytes may be anything, and 0 * NaN is NaN).  Keys that no
-      // row sees are masked, so only the others count.
-      auto put_checked = [&](const Raw16& r, uint8_t* dst, bool is_v, int t0, bool there) {
-        uint32_t far = 0;
-#pragma unroll 1
-        for (int j = 0; j < 8; ++j) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (e == j) x = r.x[e];
-          uint32_t w[4] = {x.x, x.y, x.z, x.w};
-          const int t = t0 + 2 * j + rh;
-          const bool seen = there && t <= b_last && (t >= low0 || t < sinks);
-          bool big = false;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const bool lo = (w[e] & 0x7FFFu) >= kBf16Limit, hi = (w[e] >> 16 & 0x7FFFu) >= kBf16Limit;
-            big = big || lo || hi;
-            w[e] &= (lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0x0000FFFFu : 0xFFFFFFFFu);
-          }
-          const uint32_t m = __ballot_sync(0xffffffffu, big && seen);
-          far |= ((m & 0xFFFFu ? 1u : 0u) | (m >> 16 ? 2u : 0u)) << (2 * j);
-          uint4 y = make_uint4(bf16x2_to_f16x2(w[0]), bf16x2_to_f16x2(w[1]), bf16x2_to_f16x2(w[2]), bf16x2_to_f16x2(w[3]));
-          if (is_v && !seen) y = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(dst + j * 256 + (((ch & 7) ^ ((2 * j + rh) & 7)) << 4)) = y;
-        }
-        return far;
-      };
-      auto all_seen = [&](int t0, bool there) {
-        return there && t0 + 15 <= b_last && (t0 >= low0 || t0 + 16 <= sinks);
-      };
-      for (int g = id - count; ok && g < items; g += count) {
-        const int gk = g + count, itk = gk >> 3, stk = itk % kStages, it = g >> 3, st = it % kStages;
-        const bool has_k = gk < items, has_v = g >= 0;
-        if (has_k) ok = free_k(itk);
-        if (has_v) ok = ok && free_v(it);
-        if (!ok) break;
-        uint32_t fk = 0, fv = 0;
-        const int kpage = has_v ? next : page;
-        if (has_k) {
-          uint8_t* dst = dst0 + stk * kStageBytes + (gk & 7) * 2048;
-          const int t0 = tile_at(itk) * kKeys + 16 * (gk & 7);
-          if (__any_sync(0xffffffffu, put(k, dst))) fk = put_checked(k, dst, false, t0, page_ok(kv, kpage));
-        }
-        if (has_v) {
-          uint8_t* dst = dst0 + st * kStageBytes + 2 * kHalf + (g & 7) * 2048;
-          const int t0 = tile_at(it) * kKeys + 16 * (g & 7);
-          if (__any_sync(0xffffffffu, put(v, dst)) || !all_seen(t0, page_ok(kv, page)))
-            fv = put_checked(v, dst, true, t0, page_ok(kv, page));
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-          if (has_k) {
-            mapped[itk & 7][gk & 7] = page_ok(kv, kpage);
-            odd[0][itk & 7][gk & 7] = (uint16_t)fk;
-            mbar_arrive(&k_full[stk]);
-          }
-          if (has_v) {
-            odd[1][it & 7][g & 7] = (uint16_t)fv;
-            mbar_arrive(&v_full[st]);
-          }
-        }
-        const int nk = has_v ? after : next;
-        load_rows(kb, stride, nk, page_ok(kv, nk), k);
-        if (has_v) {
-          load_rows(vb, stride, next, page_ok(kv, next), v);
-          page = next;
-          next = after;
-          after = page_of(gk + 2 * count);
-        }
+      // K of the step after; V of the item whose K was just unpacked
+      load(kb, has_v ? after : next, k);
+      if (has_v) {
+        load(vb, next, v);
+        page = next;
+        next = after;
+        after = page_of(gk + 2 * kUnpackWarps);
       }
     }
     if (!ok && lane == 0) atomicOr(status, SPEC_ST_DEVICE_WAIT);
   };
-  // softmax warps without rows unpack as well
-  const int unpackers = kUnpackWarps + 2 * (4 - row_warps);
 
   // (total == 0: nothing of this chunk is seen)
   if (warp >= kSoftWarps) {
-  if constexpr (k4)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
-  else
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n");
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
   if (total == 0) {
   } else if (warp >= kWLoad) {
-    unpack(warp - kWLoad, unpackers);
+    unpack(warp - kWLoad);
   } else if (warp == kWQk) {
     // ------------------------------------------------------------ S = Q . K^T
     // D f32 (bit 4), A and B f16, N >> 3 at 17, M >> 4 at 24; 8 d steps of 16,
@@ -438,22 +315,15 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
     if (last >= 0) mbar_wait(&pv_done[last & 1], (last >> 1) & 1);
   }
   } else {
-  if constexpr (k4)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n");
-  else
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;\n");
-  if (total == 0) {
-  } else if ((warp & 3) >= row_warps) {
-    unpack(kUnpackWarps + (warp >> 2) * (4 - row_warps) + (warp & 3) - row_warps, unpackers);
-  } else {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 184;\n");
+  if (total > 0 && (warp & 3) < row_warps) {
     // ------------------------------------------------------------ softmax
     const int h = warp >> 2, ww = warp & 3;
     const int r = 32 * ww + lane, fr = r0 + r;          // tile row, row of the KV head
     const bool live = r < nr;
-    const int i = live ? div24(fr, pl.group) : 0, hd = live ? fr - i * pl.group : 0;
+    const int i = live ? div24(fr, pl.group) : 0;
     const uint32_t tl = tmem + ((uint32_t)(32 * ww) << 16);
     constexpr float kBias = 7.f;                        // p = 2^(7 + s - max): binary16 keeps 2^-24 of 2^7
-    const float* qr = q + ((size_t)i * pl.nq + kvh * pl.group + hd) * 128;
     // one lane arrives for the warp: the warp barrier orders the others' writes
     auto arrive = [&](uint64_t* bar) {
       __syncwarp();
@@ -468,7 +338,8 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
       float mx = 0.f;
 #pragma unroll
       for (int d = 0; d < 16; ++d) {
-        y[d] = live ? reinterpret_cast<const float4*>(qr)[16 * h + d] : make_float4(0.f, 0.f, 0.f, 0.f);
+        y[d] = live ? *reinterpret_cast<const float4*>(q_rows + 512 * r + (((16 * h + d) ^ (r & 7)) << 4))
+                    : make_float4(0.f, 0.f, 0.f, 0.f);
         mx = fmaxf(mx, fmaxf(fmaxf(fabsf(y[d].x), fabsf(y[d].y)), fmaxf(fabsf(y[d].z), fabsf(y[d].w))));
       }
       pair[h][r] = mx;
@@ -521,7 +392,7 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
       };
 #pragma unroll 1
       for (int sc = 0; sc < n; ++sc, ++it) {
-        const int sb = it & 1, st = it % kStages, t0 = tile_at(it) * kKeys;
+        const int sb = it & 1, t0 = tile_at(it) * kKeys;
         bool got = __all_sync(0xffffffffu, mbar_wait(&s_full[sb], (it >> 1) & 1));
         tc_fence_after();
         const uint32_t sa = tl + kTmS + 128u * sb + 64u * h;
@@ -533,29 +404,6 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
         const bool masked = (mp.x & mp.y) != 0x01010101u || t0 + kKeys - 1 > n_past || (t0 < low1 && t0 + kKeys > sinks) ||
                             passes > 1;
         tmem_wait_ld();
-        if (!k4) {
-          // keys with an element past binary16: their scores in fp32
-          const uint2 m = *reinterpret_cast<const uint2*>(&odd[0][it & 7][4 * h]);
-          if (m.x | m.y) {
-#pragma unroll 1
-            for (int c = 0; c < 64; ++c) {
-              if (!(((c < 32 ? m.x : m.y) >> (c & 31)) & 1u)) continue;
-              const int t = t0 + 64 * h + c;
-              const uint16_t* kr = kv.pool + ((((size_t)page_at(kv, t >> 4) * kv.n_layers + layer) * 2) * kv.n_kv + kvh) * 2048 +
-                                   (t & 15) * 128;
-              float y = 0.f;
-#pragma unroll 4
-              for (int d = 0; d < 128; ++d) y = fmaf(qr[d], __uint_as_float((uint32_t)kr[d] << 16), y);
-              y *= (1.4426950408889634f / sqrtf(128.0f)) / unit;
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                float a, b;
-                f2unpack(x[e], a, b);
-                x[e] = f2pack(2 * e == c ? y : a, 2 * e + 1 == c ? y : b);
-              }
-            }
-          }
-        }
         if (masked) {
           // keys of this thread that its row sees
 #pragma unroll
@@ -621,50 +469,6 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
         float s0, s1;
         f2unpack(sum, s0, s1);
         lsum += s0 + s1;
-        if (!k4) {
-          // V elements past binary16 are zero in the tile: their p v is added
-          // here in fp32, to the rows that see them
-          got = __all_sync(0xffffffffu, mbar_wait(&v_full[st], (it / kStages) & 1));
-          const uint4 m = *reinterpret_cast<const uint4*>(&odd[1][it & 7][0]);
-          if (!got || !ok) *reinterpret_cast<volatile int*>(&gave_up[ww]) = 1;
-          if (named_bar_or(1 + ww, 64, (m.x | m.y | m.z | m.w) != 0 || !got || !ok)) {
-            left = *reinterpret_cast<volatile int*>(&gave_up[ww]) != 0;
-            if (left) break;
-            const uint32_t mw[4] = {m.x, m.y, m.z, m.w};
-#pragma unroll 1
-            for (int k = 0; k < kKeys; ++k) {
-              if (!((mw[k >> 5] >> (k & 31)) & 1u)) continue;
-              const int t = t0 + k;
-              if ((k >> 6) == h) {
-                float y = 0.f;
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  float a, b;
-                  f2unpack(x[e], a, b);
-                  if (2 * e == (k & 63)) y = a;
-                  if (2 * e + 1 == (k & 63)) y = b;
-                }
-                pair[0][r] = mine && t <= p && (t >= plow || t < sinks) ? y : -1.f;
-              }
-              named_bar(1 + ww, 64);
-              const float y = pair[0][r];
-              const uint16_t* vr = kv.pool + ((((size_t)page_at(kv, t >> 4) * kv.n_layers + layer) * 2 + 1) * kv.n_kv + kvh) * 2048 +
-                                   (t & 15) * 128 + 64 * h;
-              if (!(y < 0.f)) {
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                  float a, b;
-                  f2unpack(acc[c], a, b);
-                  const uint32_t w0 = vr[2 * c], w1 = vr[2 * c + 1];
-                  if ((w0 & 0x7FFFu) >= kBf16Limit) a += y * __uint_as_float(w0 << 16);
-                  if ((w1 & 0x7FFFu) >= kBf16Limit) b += y * __uint_as_float(w1 << 16);
-                  acc[c] = f2pack(a, b);
-                }
-              }
-              named_bar(1 + ww, 64);
-            }
-          }
-        }
         // O may be rewritten once the tile before has been added up
         if (pending) ok = ok && drain();
         pending = true;
@@ -812,8 +616,7 @@ size_t paged_attention_floats(int nq, int nkv, int max_rows, int num_sms) {
   return (size_t)pattn_chunks(nkv, 1, num_sms) * nq * max_rows * 130;
 }
 
-template <bool k4>
-static cudaError_t launch_pattn(const PattnPlan& pl, const KvView& kv, int layer, const float* q, int row_tiles,
+static cudaError_t launch_pattn_kv4(const PattnPlan& pl, const KvView& kv, int layer, const float* q, int row_tiles,
                                 float* part_o, float2* part_ml, int32_t* status, cudaStream_t st) {
   // the shared-memory limit is a per-device attribute
   constexpr int kMaxDevices = 64;
@@ -823,11 +626,11 @@ static cudaError_t launch_pattn(const PattnPlan& pl, const KvView& kv, int layer
   if (e != cudaSuccess) return e;
   const bool known = dev >= 0 && dev < kMaxDevices;
   if (!known || !have[dev]) {
-    e = cudaFuncSetAttribute(pattn_kernel<k4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPattnSmem);
+    e = cudaFuncSetAttribute(pattn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPattnSmem);
     if (e != cudaSuccess) return e;
     if (known) have[dev] = true;
   }
-  pattn_kernel<k4><<<dim3(pl.slots, pl.nkv, row_tiles), kPattnThreads, kPattnSmem, st>>>(q, pl, kv, layer, part_o, part_ml,
+  pattn_kernel<<<dim3(pl.slots, pl.nkv, row_tiles), kPattnThreads, kPattnSmem, st>>>(q, pl, kv, layer, part_o, part_ml,
                                                                                         status);
   return cudaGetLastError();
 }
@@ -861,7 +664,7 @@ cudaError_t launch_paged_attention(bool k4, const KvView& kv, int layer, const f
   float2* ml = reinterpret_cast<float2*>(part);        // [slots][nkv][R], then the outputs
   float* po = part + 2 * (size_t)pl.C * nq * 16;
   cudaError_t e = R <= kFewRows ? launch_pattn_few(k4, pl, kv, layer, q, po, ml, st)
-                  : k4          ? launch_pattn<true>(pl, kv, layer, q, row_tiles, po, ml, status, st)
+                  : k4          ? launch_pattn_kv4(pl, kv, layer, q, row_tiles, po, ml, status, st)
                                 : launch_pattn_bf16(pl, kv, layer, q, row_tiles, po, ml, status, st);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];

@@ -48,16 +48,6 @@ struct FewRing {
   static constexpr int kWarp = kSlots * (kK + kV);
   static constexpr size_t kSmem = kFewWarps * kWarp > kFewOBytes ? kFewWarps * kWarp : kFewOBytes;
 };
-// 16 bytes global -> shared, completion by group
-SPEC_DEV void copy16(uint8_t* dst, const uint8_t* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-SPEC_DEV void copy_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-template <int kPending>
-SPEC_DEV void copy_wait() {
-  asm volatile("cp.async.wait_group %0;\n" ::"n"(kPending) : "memory");
-}
-
 template <bool k4>
 SPEC_DEV void mma16816(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
   if constexpr (k4)
@@ -74,9 +64,7 @@ template <bool k4>
 SPEC_DEV uint32_t take_part(float& x0, float& x1) {
   if constexpr (k4) {
     const __half2 h = __floats2half2_rn(x0, x1);
-    const float2 f = __half22float2(h);
-    x0 -= f.x;
-    x1 -= f.y;
+    minus_f16x2(x0, x1, *reinterpret_cast<const uint32_t*>(&h));
     return *reinterpret_cast<const uint32_t*>(&h);
   } else {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
@@ -101,7 +89,8 @@ SPEC_DEV uint32_t e2m1_byte(uint32_t w) {
 SPEC_DEV uint32_t e2m1_pick(uint32_t w, int b) {        // b known at compile time after unrolling
   return b == 0 ? e2m1_byte<0>(w) : (b == 1 ? e2m1_byte<1>(w) : (b == 2 ? e2m1_byte<2>(w) : e2m1_byte<3>(w)));
 }
-SPEC_DEV uint32_t scale_pair(uint32_t byte) { return min(byte, (uint32_t)kKv4TopScale) * 0x00800080u; }
+// the scale of a byte in both halves
+SPEC_DEV uint32_t scale_pair(uint32_t byte) { return byte * 0x00800080u; }
 
 template <bool k4>
 __global__ void __launch_bounds__(32 * kFewWarps, 1)
@@ -270,8 +259,8 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
         uint32_t ksc[2][2], ks_word = 0, vs_word = 0;   // word `lane` of the scales: groups 4 (lane % 2).. of key lane / 2
         uint4 kc[2];
         if constexpr (k4) {
-          ks_word = *reinterpret_cast<const uint32_t*>(kp + 4 * 288 + 4 * lane);
-          vs_word = *reinterpret_cast<const uint32_t*>(vp + 4 * 288 + 4 * lane);
+          ks_word = __vminu4(*reinterpret_cast<const uint32_t*>(kp + 4 * 288 + 4 * lane), 0x01010101u * kKv4TopScale);
+          vs_word = __vminu4(*reinterpret_cast<const uint32_t*>(vp + 4 * 288 + 4 * lane), 0x01010101u * kKv4TopScale);
           // scales 2 g and 2 g + 1 of this lane's keys
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt) {

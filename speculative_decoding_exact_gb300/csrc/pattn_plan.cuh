@@ -79,9 +79,16 @@ SPEC_DEV TileList tiles_of(const Span& s, int c) {
   return t;
 }
 
+// x0 and x1 less the halves of a binary16 pair
+SPEC_DEV void minus_f16x2(float& x0, float& x1, uint32_t h) {
+  asm("{\n .reg .f16 a, b, m;\n mov.b32 {a, b}, %2;\n mov.b16 m, 0xBC00U;\n"      // m = -1
+      " fma.rn.f32.f16 %0, a, m, %0;\n fma.rn.f32.f16 %1, b, m, %1;\n}\n"
+      : "+f"(x0), "+f"(x1)
+      : "r"(h));
+}
 SPEC_DEV uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
 
-// loads issued where they stand (a plain load may be moved down to its use,
+// a load issued where it stands (a plain load may be moved down to its use,
 // behind a wait)
 SPEC_DEV uint4 ldg_now(const uint4* p) {
   uint4 v;
@@ -90,11 +97,26 @@ SPEC_DEV uint4 ldg_now(const uint4* p) {
                : "l"(p));
   return v;
 }
+SPEC_DEV uint2 ldg_now(const uint2* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
 SPEC_DEV uint32_t ldg_now(const void* p) {
   uint32_t v;
   asm volatile("ld.global.nc.u32 %0, [%1];\n" : "=r"(v) : "l"(p));
   return v;
 }
+// 16 bytes global -> shared, completion by group
+SPEC_DEV void copy16(uint8_t* dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+SPEC_DEV void copy_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int kPending>
+SPEC_DEV void copy_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(kPending) : "memory");
+}
+
 // the page id of a logical page, -1 past the table; to be checked where it is
 // used (a check here would wait for the load)
 SPEC_DEV int page_at(const KvView& kv, int lp) {
