@@ -36,17 +36,12 @@
 #include "attn_mma.cuh"
 #include "common.cuh"
 #include "internal.h"
-#include "kv4.cuh"
 #include "pattn_plan.cuh"
+#include "pattn_unpack.cuh"
 
 namespace spec {
 
-constexpr int kHalf = kKeys * 128;                  // one d half of a K or V tile: [keys][64 values]
-constexpr int kStageBytes = 4 * kHalf;              // K then V, 64 KB
-
-constexpr int kStages = 3;                          // [d half][key][128 B], 128-byte swizzle; K, then V
 constexpr int kUnpackWarps = 6;
-constexpr int kItemsPerTile = kPagesPerTile / 2;    // what an unpacking warp takes at once: two pages, 32 keys
 constexpr size_t kPattnSmem = 1024 + (size_t)kStages * kStageBytes;
 // TMEM columns: two score buffers, each overwritten in place by its P parts
 // (16 columns of high and 16 of low parts per 32 keys); O; Q (64 columns of high
@@ -87,42 +82,6 @@ SPEC_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
 }
 
-// One key of K or V: codes and scale bytes
-struct Raw4 {
-  uint4 c[4];
-  uint2 s;
-};
-// p: the page's chunk 0 of the key; scales: from there to its scale bytes
-SPEC_DEV void load_key(const uint8_t* p, int scales, bool there, Raw4& r) {
-  if (!there) {                                          // unmapped: zeros (its keys are masked)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) r.c[c] = make_uint4(0, 0, 0, 0);
-    r.s = make_uint2(0, 0);
-    return;
-  }
-#pragma unroll
-  for (int c = 0; c < 4; ++c) r.c[c] = ldg_now(reinterpret_cast<const uint4*>(p + 256 * c));
-  r.s = ldg_now(reinterpret_cast<const uint2*>(p + scales));
-}
-// the 128 values of a key as binary16 into its row of the tile's d halves (128
-// bytes each, 16-byte chunk j at j ^ (row % 8)); the eight lanes of a store phase
-// hold different rows % 8, so no two meet in a bank
-SPEC_DEV void unpack_key(const Raw4& r, uint8_t* row, int r7) {
-  const uint32_t sc[2] = {__vminu4(r.s.x, 0xE2E2E2E2u), __vminu4(r.s.y, 0xE2E2E2E2u)};
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const uint32_t w[4] = {r.c[c].x, r.c[c].y, r.c[c].z, r.c[c].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t s2 = ((sc[c >> 1] >> (8 * (2 * (c & 1) + (j >> 1)))) & 0xFFu) * 0x00800080u;   // (byte << 7) in both halves
-      uint32_t f[4];
-      e2m1_word(w[j], f);
-      *reinterpret_cast<uint4*>(row + (c >> 1) * kHalf + (((4 * (c & 1) + j) ^ r7) << 4)) =
-          make_uint4(hmul2_u32(f[0], s2), hmul2_u32(f[1], s2), hmul2_u32(f[2], s2), hmul2_u32(f[3], s2));
-    }
-  }
-}
-
 // ---------------------------------------------------------------------------
 // partials: grid (slot, KV head, row tile)
 // ---------------------------------------------------------------------------
@@ -132,8 +91,8 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
   extern __shared__ __align__(128) uint8_t dsm[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~(uintptr_t)1023);
   __shared__ uint32_t tmem_slot;
-  __shared__ __align__(8) uint64_t q_full, k_full[kStages], v_full[kStages], k_free[kStages], v_free[kStages],
-      s_full[2], p_full[2], pv_done[2];
+  __shared__ __align__(8) uint64_t q_full, s_full[2], p_full[2], pv_done[2];
+  __shared__ __align__(8) StageBars bar;
   __shared__ float pair[2][128];                        // what the two threads of a row exchange
   // mapped pages per tile (a ring of 8: a tile's entries are rewritten eight tiles
   // later, when its softmax has long been passed)
@@ -148,10 +107,10 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
   if (tid == 32 * kWPv) {
     mbar_init(&q_full, 2 * row_warps);
     for (int b = 0; b < kStages; ++b) {
-      mbar_init(&k_full[b], kItemsPerTile);
-      mbar_init(&v_full[b], kItemsPerTile);
-      mbar_init(&k_free[b], 1);
-      mbar_init(&v_free[b], 1);
+      mbar_init(&bar.k_full[b], kItemsPerTile);
+      mbar_init(&bar.v_full[b], kItemsPerTile);
+      mbar_init(&bar.k_free[b], 1);
+      mbar_init(&bar.v_free[b], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&s_full[b], 1);
@@ -189,67 +148,14 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  // ---------------------------------------------------------------- unpack
-  // Item g is pages 2 (g % 4) and the next of tile g / 4, a key per lane; warp id
-  // takes every kUnpackWarps-th.  A step waits, unpacks and signals for K of one
-  // item and V of the item before (whose stage is freed later).  The registers hold
-  // the next step's keys.  (With items of one page, where the bookkeeping weighs
-  // more than the unpacking, 208 rows over 32k keys took 43 instead of 39 us;
-  // filling slots in shared memory by cp.async two steps ahead was no faster.)
-  auto unpack = [&](int id) {
-    const int items = total * kItemsPerTile;
-    auto page_of = [&](int g) {
-      return g < items ? page_at(kv, tile_at(g / kItemsPerTile) * kPagesPerTile + 2 * (g % kItemsPerTile) + (lane >> 4)) : -1;
-    };
-    const uint32_t stride = (uint32_t)(kv.n_layers * 2 * kv.n_kv) * kKv4PageBytes;
-    const int t = lane & 15, scales = kKv4Scales + 8 * t - 16 * t;
-    const uint8_t* kb = reinterpret_cast<const uint8_t*>(kv.pool) + (size_t)(layer * 2 * kv.n_kv + kvh) * kKv4PageBytes + 16 * t;
-    const uint8_t* vb = kb + kv.n_kv * kKv4PageBytes;
-    auto load = [&](const uint8_t* base, int page, Raw4& r) {
-      load_key(base + (uint64_t)(uint32_t)page * stride, scales, page_ok(kv, page), r);
-    };
-    // the pages of this V, of this step's K, and of the K after that
-    int page = page_of(id), next = page_of(id + kUnpackWarps), after = page_of(id + 2 * kUnpackWarps);
-    bool ok = true;
-    Raw4 k, v;
-    load(kb, page, k);
-    load(vb, page, v);
-    for (int g = id - kUnpackWarps; ok && g < items; g += kUnpackWarps) {
-      const int gk = g + kUnpackWarps, itk = gk / kItemsPerTile, stk = itk % kStages, it = g / kItemsPerTile, st = it % kStages;
-      const bool has_k = gk < items, has_v = g >= 0;
-      // the stage, once its former K (V) has been read
-      if (has_k && itk >= kStages) ok = mbar_wait(&k_free[stk], ((itk / kStages) - 1) & 1);
-      if (has_k && itk == kStages - 1) ok = mbar_wait(&q_full, 0);      // Q's rows lay in this stage
-      if (has_v && it >= kStages) ok = ok && mbar_wait(&v_free[st], ((it / kStages) - 1) & 1);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      if (has_k) unpack_key(k, sm + stk * kStageBytes + (gk % kItemsPerTile) * 4096 + lane * 128, lane & 7);
-      if (has_v) unpack_key(v, sm + st * kStageBytes + 2 * kHalf + (g % kItemsPerTile) * 4096 + lane * 128, lane & 7);
-      fence_proxy_async();
-      if (has_k && t == 0) mapped[itk & 7][2 * (gk % kItemsPerTile) + (lane >> 4)] = page_ok(kv, has_v ? next : page);
-      __syncwarp();
-      if (lane == 0) {
-        if (has_k) mbar_arrive(&k_full[stk]);
-        if (has_v) mbar_arrive(&v_full[st]);
-      }
-      // K of the step after; V of the item whose K was just unpacked
-      load(kb, has_v ? after : next, k);
-      if (has_v) {
-        load(vb, next, v);
-        page = next;
-        next = after;
-        after = page_of(gk + 2 * kUnpackWarps);
-      }
-    }
-    if (!ok && lane == 0) atomicOr(status, SPEC_ST_DEVICE_WAIT);
-  };
-
   // (total == 0: nothing of this chunk is seen)
   if (warp >= kSoftWarps) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
   if (total == 0) {
   } else if (warp >= kWLoad) {
-    unpack(warp - kWLoad);
+    // Q's rows lie in the last stage until they have been read
+    if (!unpack_tiles<kUnpackWarps>(warp - kWLoad, total, tile_at, kv, layer, kvh, sm, bar, mapped, &q_full) && lane == 0)
+      atomicOr(status, SPEC_ST_DEVICE_WAIT);
   } else if (warp == kWQk) {
     // ------------------------------------------------------------ S = Q . K^T
     // D f32 (bit 4), A and B f16, N >> 3 at 17, M >> 4 at 24; 8 d steps of 16,
@@ -261,7 +167,7 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
     int last = -1;
     for (int it = 0; ok && it < total; ++it) {
       const int st = it % kStages, sb = it & 1;
-      bool w = mbar_wait(&k_full[st], (it / kStages) & 1);
+      bool w = mbar_wait(&bar.k_full[st], (it / kStages) & 1);
       // the buffer's P of two tiles ago has been read
       if (it >= 2) w = w && mbar_wait(&pv_done[sb], ((it >> 1) - 1) & 1);
       ok = __all_sync(0xffffffffu, w);
@@ -276,7 +182,7 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
             mma_f16_ts(tm + kTmS + 128u * sb, tm + kTmQ + 64u * pt + 8u * ks,
                        dk + (uint64_t)(((ks >> 2) * kHalf + (ks & 3) * 32) >> 4), kId, pt == 0 || ks != 0);
         mma_commit(&s_full[sb]);
-        mma_commit(&k_free[st]);
+        mma_commit(&bar.k_free[st]);
       }
       __syncwarp();
       last = it;
@@ -294,7 +200,7 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
     int last = -1;
     for (int it = 0; ok && it < total; ++it) {
       const int st = it % kStages, sb = it & 1;
-      ok = __all_sync(0xffffffffu, mbar_wait(&v_full[st], (it / kStages) & 1) && mbar_wait(&p_full[sb], (it >> 1) & 1));
+      ok = __all_sync(0xffffffffu, mbar_wait(&bar.v_full[st], (it / kStages) & 1) && mbar_wait(&p_full[sb], (it >> 1) & 1));
       if (!ok) break;
       tc_fence_after();
       if (elect_one()) {
@@ -306,7 +212,7 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
             mma_f16_ts(tm + kTmO, tm + kTmS + 128u * sb + 32u * (kk >> 1) + 16u * pt + 8u * (kk & 1),
                        dv + (uint64_t)((kk * 2048) >> 4), kId, pt == 0 || kk != 0);
         mma_commit(&pv_done[sb]);
-        mma_commit(&v_free[st]);
+        mma_commit(&bar.v_free[st]);
       }
       __syncwarp();
       last = it;
@@ -663,7 +569,8 @@ cudaError_t launch_paged_attention(bool k4, const KvView& kv, int layer, const f
   pl.tile_rows = (R + row_tiles - 1) / row_tiles;
   float2* ml = reinterpret_cast<float2*>(part);        // [slots][nkv][R], then the outputs
   float* po = part + 2 * (size_t)pl.C * nq * 16;
-  cudaError_t e = R <= kFewRows ? launch_pattn_few(k4, pl, kv, layer, q, po, ml, st)
+  cudaError_t e = R <= kFewRows ? (k4 ? launch_pattn_kv4_few(pl, kv, layer, q, po, ml, status, st)
+                                      : launch_pattn_few(k4, pl, kv, layer, q, po, ml, st))
                   : k4          ? launch_pattn_kv4(pl, kv, layer, q, row_tiles, po, ml, status, st)
                                 : launch_pattn_bf16(pl, kv, layer, q, row_tiles, po, ml, status, st);
   if (e != cudaSuccess) return e;
