@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libspecverify.so")
 SOURCES = ["gemm.cu", "glue.cu", "attn.cu", "sample.cu", "tree.cu", "cudacore.cu", "qkrope.cu",
-           "kv4.cu", "pattn.cu", "pattn_few.cu", "pattn_bf16.cu", "pattn_kv4_few.cu", "api.cu", "noalloc.cu"]
+           "kv4.cu", "pattn.cu", "pattn_few.cu", "pattn_bf16.cu", "api.cu", "noalloc.cu"]
 HEADERS = ["common.cuh", "internal.h", "gemm_plan.h", "quant.cuh", "kvmeta.cuh", "kv4.cuh", "attn_mma.cuh", "pattn_plan.cuh", "pattn_unpack.cuh"]
 ROOT = os.path.dirname(HERE)
 PUBLIC_HEADER = os.path.join(ROOT, "include", "spec_verify.h")

@@ -569,8 +569,7 @@ cudaError_t launch_paged_attention(bool k4, const KvView& kv, int layer, const f
   pl.tile_rows = (R + row_tiles - 1) / row_tiles;
   float2* ml = reinterpret_cast<float2*>(part);        // [slots][nkv][R], then the outputs
   float* po = part + 2 * (size_t)pl.C * nq * 16;
-  cudaError_t e = R <= kFewRows ? (k4 ? launch_pattn_kv4_few(pl, kv, layer, q, po, ml, status, st)
-                                      : launch_pattn_few(k4, pl, kv, layer, q, po, ml, st))
+  cudaError_t e = R <= kFewRows ? launch_pattn_few(k4, pl, kv, layer, q, po, ml, st)
                   : k4          ? launch_pattn_kv4(pl, kv, layer, q, row_tiles, po, ml, status, st)
                                 : launch_pattn_bf16(pl, kv, layer, q, row_tiles, po, ml, status, st);
   if (e != cudaSuccess) return e;

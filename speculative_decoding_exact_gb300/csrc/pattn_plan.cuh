@@ -160,8 +160,6 @@ constexpr int kFewRows = 16;
 cudaError_t launch_pattn_few(bool k4, const PattnPlan& pl, const KvView& kv, int layer, const float* q, float* part_o,
                              float2* part_ml, cudaStream_t st);
 
-cudaError_t launch_pattn_kv4_few(const PattnPlan& pl, const KvView& kv, int layer, const float* q, float* part_o,
-                                 float2* part_ml, int32_t* status, cudaStream_t st);
 // attention over a bf16 cache for more rows
 cudaError_t launch_pattn_bf16(const PattnPlan& pl, const KvView& kv, int layer, const float* q, int row_tiles, float* part_o,
                               float2* part_ml, int32_t* status, cudaStream_t st);

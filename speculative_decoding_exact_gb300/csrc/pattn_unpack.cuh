@@ -1,5 +1,5 @@
-// pattn_unpack.cuh — pages of a 4-bit cache into the binary16 operand tiles of the
-// attention kernels (pattn.cu, pattn_few.cu).
+// pattn_unpack.cuh — pages of a 4-bit cache into the binary16 operand tiles of
+// attention for many rows (pattn.cu).
 #pragma once
 #include "common.cuh"
 #include "internal.h"
@@ -61,8 +61,8 @@ SPEC_DEV void unpack_key(const Raw4& r, uint8_t* row, int r7) {
 // where the bookkeeping weighs more than the unpacking, 208 rows over 32k keys took
 // 43 instead of 39 us; filling slots in shared memory by cp.async two steps ahead
 // was no faster.)
-// mapped: per tile mod 8 and page, whether it is; last_stage: if not NULL, to be
-// waited for before the last stage is first written.  False when a wait ran out.
+// mapped: per tile mod 8 and page, whether it is; last_stage: to be waited for
+// before the last stage is first written.  False when a wait ran out.
 template <int kWarps, class TileAt>
 SPEC_DEV bool unpack_tiles(int id, int total, TileAt tile_at, const KvView& kv, int layer, int kvh, uint8_t* stages,
                            StageBars& bar, uint8_t (*mapped)[kPagesPerTile], uint64_t* last_stage) {
@@ -89,7 +89,7 @@ SPEC_DEV bool unpack_tiles(int id, int total, TileAt tile_at, const KvView& kv, 
     const bool has_k = gk < items, has_v = g >= 0;
     // the stage, once its former K (V) has been read
     if (has_k && itk >= kStages) ok = mbar_wait(&bar.k_free[stk], ((itk / kStages) - 1) & 1);
-    if (last_stage && has_k && itk == kStages - 1) ok = mbar_wait(last_stage, 0);
+    if (has_k && itk == kStages - 1) ok = mbar_wait(last_stage, 0);
     if (has_v && it >= kStages) ok = ok && mbar_wait(&bar.v_free[st], ((it / kStages) - 1) & 1);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
