@@ -126,13 +126,20 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
   // the rows of Q, whole rows by a warp, into the last stage (which tile 2 is the
   // first to use), 16-byte chunk j at j ^ (row % 8)
   uint8_t* q_rows = sm + (kStages - 1) * kStageBytes;
+  {
+    constexpr int kRows = 128 / (kPattnThreads / 32);
+    const int fr = r0 + kRows * warp;
+    int i = div24(fr, pl.group), hd = fr - i * pl.group;
 #pragma unroll
-  for (int j = 0; j < 128 / (kPattnThreads / 32); ++j) {
-    const int r = warp + (kPattnThreads / 32) * j, fr = r0 + r;
-    if (r < nr) {
-      const int i = div24(fr, pl.group);
-      copy16(q_rows + 512 * r + ((lane ^ (r & 7)) << 4),
-             reinterpret_cast<const uint8_t*>(q + ((size_t)i * pl.nq + kvh * pl.group + fr - i * pl.group) * 128) + 16 * lane);
+    for (int j = 0; j < kRows; ++j) {
+      const int r = kRows * warp + j;
+      if (r < nr)
+        copy16(q_rows + 512 * r + ((lane ^ (r & 7)) << 4),
+               reinterpret_cast<const uint8_t*>(q + ((size_t)i * pl.nq + kvh * pl.group + hd) * 128) + 16 * lane);
+      if (++hd == pl.group) {
+        hd = 0;
+        ++i;
+      }
     }
   }
   copy_commit();

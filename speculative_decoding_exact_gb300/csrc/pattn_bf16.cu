@@ -101,13 +101,16 @@ pattn_bf16_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, const __
   const int qw = warp < kWLoadK ? warp : warp - 2;
   float4 y[kQRows];
   if (warp != kWLoadK && warp != kWLoadV) {
+    const int fr = r0 + kQRows * qw;
+    int i = div24(fr, pl.group), hd = fr - i * pl.group;
 #pragma unroll
     for (int j = 0; j < kQRows; ++j) {
-      const int r = qw + kQWarps * j, fr = r0 + r;
       y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < nr) {
-        const int i = div24(fr, pl.group);
-        y[j] = reinterpret_cast<const float4*>(q + ((size_t)i * pl.nq + kvh * pl.group + fr - i * pl.group) * 128)[lane];
+      if (kQRows * qw + j < nr)
+        y[j] = reinterpret_cast<const float4*>(q + ((size_t)i * pl.nq + kvh * pl.group + hd) * 128)[lane];
+      if (++hd == pl.group) {
+        hd = 0;
+        ++i;
       }
     }
   }
@@ -151,7 +154,7 @@ pattn_bf16_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, const __
   } else if (total > 0) {
 #pragma unroll
     for (int j = 0; j < kQRows; ++j) {
-      const int r = qw + kQWarps * j;
+      const int r = kQRows * qw + j;
       if (r >= 32 * row_warps) break;
       uint8_t* dst = sm + (lane >> 4) * kHalf + r * 128 + ((((lane & 15) >> 1) ^ (r & 7)) << 4) + 8 * (lane & 1);
 #pragma unroll
