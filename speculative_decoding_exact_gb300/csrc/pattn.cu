@@ -5,34 +5,42 @@
 // t > p - window or t < sinks (window 0: every t <= p).
 // s_t = q.k_t / sqrt(128), o = sum_t exp(s_t - m) v_t / sum_t exp(s_t - m).
 //
-// Calls with at most 16 query rows per KV head go to pattn_few.cu.
-//
 // Decomposition (flash-decoding).  The M * group query rows of a KV head (group
-// query heads read it) are packed into tiles of up to 128 rows, the rows of the
-// tcgen05 MMAs.  Keys are taken in tiles of 128 at absolute positions:
-//   S[128 x 128 keys] = Q[128 x 128 d] . K^T      (A = Q in TMEM, B = K)
-//   O[128 x 128 d]    = P[128 x 128 keys] . V     (A = P in TMEM, B = V)
-// with a running (max, sum) per row.  A CTA (slot, KV head, row tile) walks one
-// chunk of L key tiles and writes (O, max, sum); a merge kernel joins the chunks.
-// Q and P live in TMEM because shared memory is the busiest unit: a tile's K
-// and V are written once and read twice, 192 KB.  With the keys on the MMA's
-// rows and Q and P in shared memory (a tile's work then follows the number of
-// query rows), 208 rows over 32k keys took 100 us instead of 57.
+// query heads read it) are packed into tiles of up to 128 rows.  Keys are taken in
+// tiles of 128 at absolute positions, and chunks of L tiles are worked on by one
+// CTA each (slot, KV head, row tile) with a running (max, sum) per row; a merge
+// kernel joins the chunks.
+// Three kernels write the chunks' (O, max, sum): pattn_few.cu for at most 16 query
+// rows per KV head, and for more the one here (4-bit) or pattn_bf16.cu.
 //
 // The split of the keys is a function of the row's own position and the number of
 // row tiles (chunk_len, pattn_plan.cuh): chunks are whole multiples of L tiles
 // from position 0, so a row has the same bits in every block of as many row tiles
 // (batch-height invariance).  L grows with the position such that there are never
-// more chunks than SMs per KV head and row tile; a block that crosses such a step runs its two groups of rows one after the
-// other.  Tiles that no row sees are skipped: they would add exact zeros.
+// more chunks than SMs per KV head and row tile; a block that crosses such a step
+// runs its two groups of rows one after the other.  Tiles that no row sees are
+// skipped: they would add exact zeros.
 //
-// Precision: all operands are binary16.  A 4-bit value is exact in it; a bf16
-// value is exact when 2^-17 <= |x| < 2^16 (below: off by at most 2^-25 absolute;
-// larger and non-finite elements are worked on in fp32, see `odd` below).  q and
-// p are split into two parts, 22 significant bits.  The tensor core truncates
-// its additions, so the small parts go first, and each tile's O starts afresh
-// and is added up in fp32 registers: left in TMEM over 27 tiles it was off by
-// 8e-6.
+// The 4-bit kernel for many rows, on tcgen05:
+//   S[128 x 128 keys] = Q[128 x 128 d] . K^T      (A = Q in TMEM, B = K)
+//   O[128 x 128 d]    = P[128 x 128 keys] . V     (A = P in TMEM, B = V)
+// Pages are unpacked into binary16 tiles in shared memory.  Q and P live in TMEM:
+// with the keys on the MMA's rows and Q and P in shared memory, which then carries
+// 192 KB and more per tile, 208 rows over 32k keys took 100 us when this layout
+// took 57.
+//
+// What bounds it: 32 MMAs of 128 x 128 x 16 take 2,600 cycles a tile, the softmax
+// and the unpacking 8,400 warp instructions (2,100 cycles of four schedulers at
+// best, 47 % of the slots are used): 3,200 cycles a tile.  A call of one tile per
+// CTA is latency: 3,000 cycles to the sequence length and the plan, 4,700 to page
+// ids, pages and the unpacked K, 3,900 for the tile, 2,500 to store.  16 rows of 52
+// heads on 4: 14.4 us behind 2k keys, 37.7 behind 32k (370 TFLOP/s, counting each
+// product once; two parts make it two).
+//
+// Precision: all operands are binary16.  A 4-bit value is exact in it; q and p are
+// split into two parts, 22 significant bits.  The tensor core truncates its
+// additions, so the small parts go first, and each tile's O starts afresh and is
+// added up in fp32 registers: left in TMEM over 27 tiles it was off by 8e-6.
 #include "attn_mma.cuh"
 #include "common.cuh"
 #include "internal.h"

@@ -2,23 +2,29 @@
 // of at most 16 query rows per KV head: one decoded token of a group of up to 16
 // heads, a few rows of smaller groups.
 //
-// What bounds it.  A key tile is 18 KB (4-bit) or 64 KB (bf16), 800 or 2,850 cycles
-// of an SM's share of HBM.  The tcgen05 kernel pays for 128 rows whatever their
-// number, and for unpacking the tile into shared memory; it is bound by
-// instruction issue, at 4,000 cycles a tile.  Here the 16 rows are one m16n8k16
-// fragment, and the pages go from global memory into registers in the order of
-// the MMA's B fragment, with no shared memory and no barrier on the way: 512
-// (bf16: 768) warp MMAs a tile, 2.02 cycles each per SM.
+// The tcgen05 kernels pay for 128 rows whatever their number.  Here the 16 rows are
+// one m16n8k16 fragment: 512 (bf16: 768) warp MMAs a tile of 128 keys.
 //
-// The warps of a CTA (slot, KV head) take the pages of its chunk in turn, with
-// a running (max, sum) and O of their own in registers; they are joined in order
-// at the end.  A page falls to the warp of its number mod 8, so a row's bits do
-// not depend on the block.
+// The warps of a CTA (slot, KV head) take the pages of its chunk in turn, with a
+// running (max, sum) and O of their own in registers; they are joined in order at
+// the end.  A page falls to the warp of its number mod kFewWarps, so a row's bits
+// do not depend on the block.  Each warp has a ring of pages in shared memory that
+// it fills by cp.async (16 bytes per lane; bulk copies to padded places are issued
+// lane by lane and cost 150 instructions a page).
+//
+// What bounds it: instruction issue.  A 4-bit page is 596 warp instructions, 64 of
+// them MMAs of 8 cycles; three warps per scheduler fill 49 % of the slots, 2,400
+// cycles a tile against 800 at the SM's share of HBM.  One token of 52 heads on 4
+// behind 128k keys: 43 us in 4 bits, 59 in bf16; 10.3 us behind 2k keys, of which
+// the second launch is 4.  (8 warps: 45; 16 warps, 128 registers each: 43, and 12
+// behind 2k keys.  Pages loaded into registers in fragment order: 52.  Keys on the
+// 128 rows of tcgen05 MMAs and query rows as columns: 42, with twice the code.)
 //
 // The d's of a K row and the d's and keys of a V page may be visited in any
 // order.  Lane 4n + g (g < 4) takes d's 32 g .. of K (one 16-byte chunk of codes, 64
 // bytes of bf16), and d's 16 n .. of keys 4 g .. of V:
-//   S: B fragment of MMA ks: elements 4 ks .. 4 ks + 3 of the lane's chunk; column n
+//   S: B fragment of MMA ks: elements 4 ks .. 4 ks + 3 of the lane's chunk (bf16:
+//      with its 16-byte pieces in the order c ^ (g / 2), for the banks); column n
 //      of key tile nt (of two) is key 4 (n / 2) + n % 2 + 2 nt, so that a lane's
 //      scores are those of keys 4 g .. 4 g + 3, its V rows
 //   O: column n of MMA j is d 16 n + j
@@ -142,7 +148,7 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
   const uint8_t* kbase = reinterpret_cast<const uint8_t*>(kv.pool) + (size_t)(layer * 2 * kv.n_kv + kvh) * kPageBytes;
   const uint8_t* vbase = kbase + (size_t)kv.n_kv * kPageBytes;
 
-  // This warp's pages: those of the chunk whose number is `warp` mod 12.
+  // This warp's pages: those of the chunk whose number is `warp` mod kFewWarps.
   TileList tl;
   int f0, f1, c0, pages;
   auto page_no = [&](int j) {

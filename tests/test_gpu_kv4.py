@@ -281,17 +281,18 @@ def test_attention_window_and_sinks(kind, M, length, window, sinks):
     check_attention(context(26, 2), kind, M, length, window, sinks, seed=length + window % 97)
 
 
+@pytest.mark.parametrize("nq,M", [(4, 2), (26, 9)])
 @pytest.mark.parametrize("kind", KINDS)
-def test_attention_long_and_peaked(kind):
+def test_attention_long_and_peaked(kind, nq, M):
     """Many tiles in one chunk, scores far apart (the running maximum moves) and
     keys sorted so that it moves often; large and small queries."""
-    ctx = context(4, 2, max_ctx=40000)
+    ctx = context(nq, 2, max_ctx=40000)
     for q_scale, spread in ((1.0, 1.0), (8.0, 4.0), (1e-3, 1.0)):
-        check_attention(ctx, kind, 2, 33000, 0, 0, seed=5, spread=spread, q_scale=q_scale)
+        check_attention(ctx, kind, M, 33000, 0, 0, seed=5, spread=spread, q_scale=q_scale)
     cfg = ctx.cfg
     kv, k, v, ids = cache(ctx, kind, 20000, 9)
     # one direction grows along the sequence
-    q = np.zeros((1, cfg.n_q_heads, 128), dtype=np.float32)
+    q = np.zeros((M - 1, cfg.n_q_heads, 128), dtype=np.float32)
     q[:, :, 3] = 60.0
     ramp = (np.arange(k.shape[0]) // 16 * 0.05).astype(np.float32)
     if kind == "kv4":
@@ -309,49 +310,52 @@ def test_attention_long_and_peaked(kind):
     assert (np.abs(got - want) <= bound).all()
 
 
+@pytest.mark.parametrize("nq", [26, 2])
 @pytest.mark.parametrize("kind", KINDS)
-def test_attention_rows_without_keys(kind):
+def test_attention_rows_without_keys(kind, nq):
     """seq_len below M: the rows before position 0 see nothing and are zero."""
-    ctx = context(26, 2)
+    ctx = context(nq, 2)
     for M, length in ((16, 5), (4, 0), (16, 1)):
         kv, k, v, _ = cache(ctx, kind, length, 3)
-        q = np.random.default_rng(4).standard_normal((M, 26, 128)).astype(np.float32)
+        q = np.random.default_rng(4).standard_normal((M, nq, 128)).astype(np.float32)
         got = attend(ctx, kv, kind, q, 0, 0)
-        want, bound = u.attention(q, k, v, 26, 0, 0, length, split=SPLIT[kind])
+        want, bound = u.attention(q, k, v, nq, 0, 0, length, split=SPLIT[kind])
         assert not got[:M - length].any()
         assert (np.abs(got - want) <= bound).all()
     assert status(ctx) == 0
 
 
+@pytest.mark.parametrize("nq", [26, 2])
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("window,sinks", [(0, 0), (90, 20)])
-def test_attention_unmapped_pages_are_not_seen(kind, window, sinks):
-    ctx = context(26, 2)
+def test_attention_unmapped_pages_are_not_seen(kind, window, sinks, nq):
+    ctx = context(nq, 2)
     kv, k, v, ids = cache(ctx, kind, 700, 11)
     bad = {1: -1, 8: -1, 15: kv.num_pages, 16: 2 ** 30, 39: -5, 43: -1}
     mapped = np.ones(700, dtype=bool)
     for lp, val in bad.items():
         kv.page_table[lp] = val
         mapped[16 * lp:16 * lp + 16] = False
-    q = np.random.default_rng(4).standard_normal((16, 26, 128)).astype(np.float32)
+    q = np.random.default_rng(4).standard_normal((16, nq, 128)).astype(np.float32)
     got = attend(ctx, kv, kind, q, window, sinks)
-    want, bound = u.attention(q, k, v, 26, window, sinks, 700, mapped=mapped, split=SPLIT[kind])
+    want, bound = u.attention(q, k, v, nq, window, sinks, 700, mapped=mapped, split=SPLIT[kind])
     assert (np.abs(got - want) <= bound).all()
     # no page at all: every row is empty
     kv.page_table.fill_(-1)
     assert not attend(ctx, kv, kind, q, window, sinks).any()
 
 
+@pytest.mark.parametrize("nq", [26, 2])
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("window,sinks", [(0, 0), (100, 5)])
-def test_attention_is_untouched_by_what_rows_do_not_see(kind, window, sinks):
+def test_attention_is_untouched_by_what_rows_do_not_see(kind, window, sinks, nq):
     """NaN, infinities and the largest numbers behind the sequence, in other
     pages, outside the window, and in block rows that an earlier row does not
     see: every row equals the clean run bit for bit where it does not see them."""
-    ctx = context(26, 2)
+    ctx = context(nq, 2)
     M, length = 16, 439
     kv, _, _, ids = cache(ctx, kind, length, 21)
-    q = np.random.default_rng(8).standard_normal((M, 26, 128)).astype(np.float32)
+    q = np.random.default_rng(8).standard_normal((M, nq, 128)).astype(np.float32)
     clean = attend(ctx, kv, kind, q, window, sinks)
     hidden = np.zeros((kv.num_pages, 16), dtype=bool)
     hidden[:] = True
@@ -386,25 +390,26 @@ def test_attention_is_untouched_by_what_rows_do_not_see(kind, window, sinks):
                 sees = see[:, t]
                 same = (got.view(np.uint32) == clean.view(np.uint32)).all(-1)
                 assert same[~sees].all()
-                g = got.reshape(M, 26, 128)[sees]
+                g = got.reshape(M, nq, 128)[sees]
                 if which == 1:
                     assert not np.isfinite(g[:, :, 77]).any()
                     rest = np.delete(g, 77, -1)
-                    assert np.array_equal(rest, np.delete(clean.reshape(M, 26, 128)[sees], 77, -1))
+                    assert np.array_equal(rest, np.delete(clean.reshape(M, nq, 128)[sees], 77, -1))
                 elif math.isnan(val):
                     assert not np.isfinite(g).any()
                 kv.pool.copy_(saved)
 
 
+@pytest.mark.parametrize("nq", [26, 2])
 @pytest.mark.parametrize("M,window,sinks", [(1, 0, 0), (16, 0, 0), (16, 100, 5), (5, 40, 200)])
-def test_attention_bf16_values_past_binary16(M, window, sinks):
+def test_attention_bf16_values_past_binary16(M, window, sinks, nq):
     """bf16 elements from 2^15 up to the type's largest, and whole tiny rows:
     what binary16 operands cannot hold is worked on in fp32."""
-    ctx = context(26, 2)
+    ctx = context(nq, 2)
     length = 400
     kv, k, v, ids = cache(ctx, "bf16", length, 71)
     rng = np.random.default_rng(9)
-    q = rng.standard_normal((M, 26, 128)).astype(np.float32)
+    q = rng.standard_normal((M, nq, 128)).astype(np.float32)
     for n, (t, which, d, val) in enumerate([(3, 1, 5, 40000.0), (3, 1, 6, -1e9), (200, 1, 0, 32768.0), (390, 1, 127, 7e4),
                                             (length - 1, 1, 64, 1e30), (130, 0, 9, 70000.0), (length - 2, 0, 8, -1e5),
                                             (131, 0, slice(None), 1e-7), (132, 1, slice(None), 1e-7),
@@ -415,7 +420,7 @@ def test_attention_bf16_values_past_binary16(M, window, sinks):
     q[:, :, 8:10] *= 1e-4          # so that the large K elements do not decide every row
     sync()
     got = attend(ctx, kv, "bf16", q, window, sinks)
-    want, bound = u.attention(q, k, v, 26, window, sinks, length, split=SPLIT["bf16"])
+    want, bound = u.attention(q, k, v, nq, window, sinks, length, split=SPLIT["bf16"])
     assert (np.abs(got - want) <= bound).all(), float((np.abs(got - want) / bound).max())
     assert status(ctx) == 0
 
@@ -727,4 +732,39 @@ def test_captured_calls_follow_the_device_length(kind):
             want, bound = u.attention(q.cpu().numpy(), k, v, 8, 150, 6, length, split=SPLIT[kind])
             assert (np.abs(out.cpu().numpy() - want) <= bound).all()
         assert status(ctx) == 0
+        ctx.close()
+
+
+def test_two_contexts_on_two_streams():
+    """Calls of two contexts in flight at once (small blocks, larger ones and the
+    bf16 cache): the same bits as one after the other."""
+    jobs = []
+    for seed in (1, 2):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            ctx = runtime.Context(config(26, 2), max_ctx=2048, stream=stream)
+            for kind in KINDS:
+                kv, _, _, _ = cache(ctx, kind, 1500, seed)
+                for M in (1, 16):
+                    q = torch.randn(M, 26, 128, device="cuda")
+                    jobs.append((ctx, kind, kv, q, [torch.empty(M, 26 * 128, device="cuda") for _ in range(2)]))
+    sync()
+
+    def call(job, which):
+        ctx, kind, kv, q, out = job
+        f = abi.spec_attention_kv4 if kind == "kv4" else abi.spec_attention_window
+        abi.check("attention", f(ctx.h, kv.struct(), 1, q.data_ptr(), q.shape[0], 700, 3, out[which].data_ptr()))
+    for job in jobs:
+        call(job, 0)
+        sync()
+    half = len(jobs) // 2
+    for _ in range(5):
+        for a, b in zip(jobs[:half], jobs[half:]):
+            call(a, 1)
+            call(b, 1)
+    sync()
+    for ctx, _, _, _, out in jobs:
+        assert torch.equal(out[0], out[1])
+        assert status(ctx) == 0
+    for ctx in {id(j[0]): j[0] for j in jobs}.values():
         ctx.close()
