@@ -5,20 +5,21 @@
 // The tcgen05 kernels pay for 128 rows whatever their number.  Here the 16 rows are
 // one m16n8k16 fragment: 512 (bf16: 768) warp MMAs a tile of 128 keys.
 //
-// The warps of a CTA (slot, KV head) take the pages of its chunk in turn, with a
-// running (max, sum) and O of their own in registers; they are joined in order at
-// the end.  A page falls to the warp of its number mod kFewWarps, so a row's bits
+// The warps of a CTA (slot, KV head) take the pages of its chunk in turn, 4-bit ones
+// two at a time, with a running (max, sum) and O of their own in registers; they are
+// joined in order at the end.  Pages fall to warps by their number, so a row's bits
 // do not depend on the block.  Each warp has a ring of pages in shared memory that
 // it fills by cp.async (16 bytes per lane; bulk copies to padded places are issued
 // lane by lane and cost 150 instructions a page).
 //
-// What bounds it: instruction issue.  A 4-bit page is 596 warp instructions, 64 of
-// them MMAs of 8 cycles; three warps per scheduler fill 49 % of the slots, 2,400
-// cycles a tile against 800 at the SM's share of HBM.  One token of 52 heads on 4
-// behind 128k keys: 43 us in 4 bits, 59 in bf16; 10.3 us behind 2k keys, of which
-// the second launch is 4.  (8 warps: 45; 16 warps, 128 registers each: 43, and 12
-// behind 2k keys.  Pages loaded into registers in fragment order: 52.  Keys on the
-// 128 rows of tcgen05 MMAs and query rows as columns: 42, with twice the code.)
+// What bounds it: the dependent steps of a few warps.  A 4-bit page is 491 warp
+// instructions, 64 of them MMAs of 8 cycles; two warps per scheduler fill 42 % of the
+// slots, 2,300 cycles a tile against 800 at the SM's share of HBM.  One token of 52
+// heads on 4 behind 128k keys: 41 us in 4 bits (one page at a time, 12 warps: 43, 596
+// instructions a page), 59 in bf16 (12 warps, 168 registers each); 10.3 us behind 2k
+// keys, of which the second launch is 4.  (Pages loaded into registers in fragment
+// order: 52.  Keys on the 128 rows of tcgen05 MMAs and query rows as columns: 42,
+// with twice the code.)
 //
 // The d's of a K row and the d's and keys of a V page may be visited in any
 // order.  Lane 4n + g (g < 4) takes d's 32 g .. of K (one 16-byte chunk of codes, 64
@@ -40,19 +41,18 @@
 
 namespace spec {
 
-constexpr int kFewWarps = 12;
 constexpr int kOPitch = 132;               // floats between rows of a warp's O in shared memory
-constexpr int kFewOBytes = 4 * kFewWarps * kFewRows * kOPitch;
 // A warp's ring of pages in shared memory.  Where a piece of 16 bytes lies keeps
 // the eight lanes of a load phase in different banks:
 //   4-bit: piece 16 c + t (chunk column c, key t) at 288 c + 16 t, then the scales
 //   bf16:  K row t at 288 t, V row t at 272 t + 16 (t / 8)
 template <bool k4>
 struct FewRing {
+  static constexpr int kWarps = k4 ? 8 : 12, kPg = k4 ? 2 : 1;      // kPg: pages of a unit
   static constexpr int kK = k4 ? 4 * 288 + 128 : 16 * 288, kV = k4 ? kK : 16 * 272 + 16;
-  static constexpr int kSlots = k4 ? 5 : 2;
-  static constexpr int kWarp = kSlots * (kK + kV);
-  static constexpr size_t kSmem = kFewWarps * kWarp > kFewOBytes ? kFewWarps * kWarp : kFewOBytes;
+  static constexpr int kSlots = k4 ? 3 : 2;
+  static constexpr int kWarp = kSlots * kPg * (kK + kV), kO = 4 * kWarps * kFewRows * kOPitch;
+  static constexpr size_t kSmem = kWarps * kWarp > kO ? kWarps * kWarp : kO;
 };
 template <bool k4>
 SPEC_DEV void mma16816(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
@@ -99,18 +99,19 @@ SPEC_DEV uint32_t e2m1_pick(uint32_t w, int b) {        // b known at compile ti
 SPEC_DEV uint32_t scale_pair(uint32_t byte) { return byte * 0x00800080u; }
 
 template <bool k4>
-__global__ void __launch_bounds__(32 * kFewWarps, 1)
+__global__ void __launch_bounds__(32 * FewRing<k4>::kWarps, 1)
 pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, float* __restrict__ part_o,
                  float2* __restrict__ part_ml) {
   constexpr int kParts = k4 ? 2 : 3;                    // of q and p
   constexpr float kBias = k4 ? 7.f : 0.f;               // p = 2^(bias + s - max)
   constexpr int kPageBytes = k4 ? kKv4PageBytes : 4096;
   using Ring = FewRing<k4>;
+  constexpr int kWarps = Ring::kWarps, kPg = Ring::kPg, kUnitsPerTile = kPagesPerTile / kPg;
   extern __shared__ __align__(128) uint8_t sm[];
   float* o_sm = reinterpret_cast<float*>(sm);           // [warp][row][kOPitch], where the rings were
   __shared__ uint4 qs[kParts][8][32];                   // A fragments
   __shared__ int qmax[kFewRows];
-  __shared__ float2 ml_sm[kFewWarps][kFewRows];
+  __shared__ float2 ml_sm[kWarps][kFewRows];
   __shared__ uint32_t poison;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = lane >> 2, g = lane & 3;
@@ -148,20 +149,29 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
   const uint8_t* kbase = reinterpret_cast<const uint8_t*>(kv.pool) + (size_t)(layer * 2 * kv.n_kv + kvh) * kPageBytes;
   const uint8_t* vbase = kbase + (size_t)kv.n_kv * kPageBytes;
 
-  // This warp's pages: those of the chunk whose number is `warp` mod kFewWarps.
+  // This warp's units of kPg pages: those of the chunk whose number is `warp` mod
+  // kWarps.
   TileList tl;
-  int f0, f1, c0, pages;
-  auto page_no = [&](int j) {
-    return j < c0 ? tl.a0 * kPagesPerTile + f0 + kFewWarps * j : tl.a1 * kPagesPerTile + f1 + kFewWarps * (j - c0);
+  int f0, f1, c0, units;
+  auto page_no = [&](int j) {                           // first page of unit j
+    return kPg * (j < c0 ? tl.a0 * kUnitsPerTile + f0 + kWarps * j : tl.a1 * kUnitsPerTile + f1 + kWarps * (j - c0));
   };
-  auto id_of = [&](int j) { return j < pages ? page_at(kv, page_no(j)) : -1; };
-  // Copies page j into slot b if it is mapped and some row of the block sees a key
-  // of it; whether it was.
-  auto fetch = [&](int j, int id, int b) {
-    if (j >= pages || !page_ok(kv, id)) return false;
-    const int k0 = 16 * page_no(j);
+  struct Ids {
+    int id[kPg];
+  };
+  auto ids_of = [&](int j) {
+    Ids r;
+#pragma unroll
+    for (int pg = 0; pg < kPg; ++pg) r.id[pg] = j < units ? page_at(kv, page_no(j) + pg) : -1;
+    return r;
+  };
+  // Copies page pg of unit j into slot b if it is mapped and some row of the block
+  // sees a key of it; whether it was.
+  auto fetch_page = [&](int j, int id, int b, int pg) {
+    if (!page_ok(kv, id)) return false;
+    const int k0 = 16 * (page_no(j) + pg);
     if (k0 > b_last || (k0 + 15 < low0 && k0 >= sinks)) return false;
-    uint8_t* dst = ring + b * (Ring::kK + Ring::kV);
+    uint8_t* dst = ring + (b * kPg + pg) * (Ring::kK + Ring::kV);
     const uint8_t* kp = kbase + (uint64_t)(uint32_t)id * stride;
     const uint8_t* vp = vbase + (uint64_t)(uint32_t)id * stride;
     if constexpr (k4) {
@@ -183,27 +193,32 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
     }
     return true;
   };
-  uint32_t have = 0;                                    // bit b: slot b holds a page, or will
-  int id_next = -1, id_after = -1;                      // ids of the two pages behind those of the ring
+  uint32_t have = 0;                                    // bit kPg b + pg: slot b holds that page, or will
+  auto fetch = [&](int j, const Ids& ids, int b) {
+    have &= ~(((1u << kPg) - 1u) << (kPg * b));
+    if (j < units) {
+#pragma unroll
+      for (int pg = 0; pg < kPg; ++pg)
+        if (fetch_page(j, ids.id[pg], b, pg)) have |= 1u << (kPg * b + pg);
+    }
+    copy_commit();
+  };
+  Ids id_next, id_after;                                // of the two units behind those of the ring
   auto start = [&](int pass) {
     tl = pass == 0 ? tl0 : tl1;
-    const int n0 = tl.n0 * kPagesPerTile, n1 = (tl.n - tl.n0) * kPagesPerTile;
-    auto first_of = [&](int from) { return (int)((unsigned)(warp + kFewWarps - (unsigned)from % kFewWarps) % kFewWarps); };
-    f0 = first_of(tl.a0 * kPagesPerTile);
-    f1 = first_of(tl.a1 * kPagesPerTile);
-    c0 = n0 > f0 ? (n0 - f0 + kFewWarps - 1) / kFewWarps : 0;
-    pages = c0 + (n1 > f1 ? (n1 - f1 + kFewWarps - 1) / kFewWarps : 0);
-    int id[Ring::kSlots];
+    const int n0 = tl.n0 * kUnitsPerTile, n1 = (tl.n - tl.n0) * kUnitsPerTile;
+    auto first_of = [&](int from) { return (int)((unsigned)(warp + kWarps - (unsigned)from % kWarps) % kWarps); };
+    f0 = first_of(tl.a0 * kUnitsPerTile);
+    f1 = first_of(tl.a1 * kUnitsPerTile);
+    c0 = n0 > f0 ? (n0 - f0 + kWarps - 1) / kWarps : 0;
+    units = c0 + (n1 > f1 ? (n1 - f1 + kWarps - 1) / kWarps : 0);
+    Ids id[Ring::kSlots];
 #pragma unroll
-    for (int b = 0; b < Ring::kSlots; ++b) id[b] = id_of(b);
-    id_next = id_of(Ring::kSlots);
-    id_after = id_of(Ring::kSlots + 1);
-    have = 0;
+    for (int b = 0; b < Ring::kSlots; ++b) id[b] = ids_of(b);
+    id_next = ids_of(Ring::kSlots);
+    id_after = ids_of(Ring::kSlots + 1);
 #pragma unroll
-    for (int b = 0; b < Ring::kSlots; ++b) {
-      if (fetch(b, id[b], b)) have |= 1u << b;
-      copy_commit();
-    }
+    for (int b = 0; b < Ring::kSlots; ++b) fetch(b, id[b], b);
   };
   start(0);
 
@@ -251,85 +266,105 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
     for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
     float ref[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
 
-    int b = 0;                                          // slot of page j
+    int b = 0;                                          // slot of unit j
 #pragma unroll 1
-    for (int j = 0; j < pages; ++j) {
+    for (int j = 0; j < units; ++j) {
       copy_wait<Ring::kSlots - 1>();
       __syncwarp();
-      if ((have >> b) & 1u) {
-        const uint8_t* kp = ring + b * (Ring::kK + Ring::kV);
+      const uint32_t there = (have >> (kPg * b)) & ((1u << kPg) - 1u);
+      if (there) {
+        const uint8_t* kp = ring + b * kPg * (Ring::kK + Ring::kV);
         const uint8_t* vp = kp + Ring::kK;
+        constexpr int kPgBytes = Ring::kK + Ring::kV;
         const int k0 = 16 * page_no(j);
         // ------------------------------------------------ S = Q . K^T
-        float s[2][2][4] = {};                          // [key tile][high part, low parts]
-        uint32_t ksc[2][2], ks_word = 0, vs_word = 0;   // word `lane` of the scales: groups 4 (lane % 2).. of key lane / 2
-        uint4 kc[2];
+        float s[kPg][2][2][4] = {};                     // [page][key tile][high part, low parts]
+        uint32_t ksc[kPg][2][2], vs_word[kPg];          // vs_word: word `lane` of V's scales, groups 4 (lane % 2).. of key lane / 2
+        uint4 kc[kPg][2];
         if constexpr (k4) {
-          ks_word = __vminu4(*reinterpret_cast<const uint32_t*>(kp + 4 * 288 + 4 * lane), 0x01010101u * kKv4TopScale);
-          vs_word = __vminu4(*reinterpret_cast<const uint32_t*>(vp + 4 * 288 + 4 * lane), 0x01010101u * kKv4TopScale);
-          // scales 2 g and 2 g + 1 of this lane's keys
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            const uint32_t w =
-                __shfl_sync(0xffffffffu, ks_word, 2 * (4 * (n >> 1) + (n & 1) + 2 * nt) + (g >> 1)) >> (16 * (g & 1));
-            ksc[nt][0] = scale_pair(w & 0xFFu);
-            ksc[nt][1] = scale_pair((w >> 8) & 0xFFu);
+          for (int pg = 0; pg < kPg; ++pg) {
+            const uint32_t ks_word =
+                __vminu4(*reinterpret_cast<const uint32_t*>(kp + pg * kPgBytes + 4 * 288 + 4 * lane), 0x01010101u * kKv4TopScale);
+            vs_word[pg] =
+                __vminu4(*reinterpret_cast<const uint32_t*>(vp + pg * kPgBytes + 4 * 288 + 4 * lane), 0x01010101u * kKv4TopScale);
+            // scales 2 g and 2 g + 1 of this lane's keys
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              const uint32_t w =
+                  __shfl_sync(0xffffffffu, ks_word, 2 * (4 * (n >> 1) + (n & 1) + 2 * nt) + (g >> 1)) >> (16 * (g & 1));
+              ksc[pg][nt][0] = scale_pair(w & 0xFFu);
+              ksc[pg][nt][1] = scale_pair((w >> 8) & 0xFFu);
+            }
           }
         }
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
-          uint32_t kb[2][2];
+          uint32_t kb[kPg][2][2];
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            const int t = 4 * (n >> 1) + (n & 1) + 2 * nt;      // this lane's key
-            if constexpr (k4) {
-              if (ks == 0) kc[nt] = *reinterpret_cast<const uint4*>(kp + 288 * g + 16 * t);
-              const uint32_t w = word_of(kc[nt], ks >> 1), s2 = ksc[nt][ks >> 2];
-              kb[nt][0] = hmul2_u32(e2m1_pick(w, 2 * (ks & 1)), s2);
-              kb[nt][1] = hmul2_u32(e2m1_pick(w, 2 * (ks & 1) + 1), s2);
-            } else {
-              if ((ks & 1) == 0)
-                kc[nt] = *reinterpret_cast<const uint4*>(kp + 288 * t + 64 * g + 16 * ((ks >> 1) ^ (g >> 1)));
-              kb[nt][0] = word_of(kc[nt], 2 * (ks & 1));
-              kb[nt][1] = word_of(kc[nt], 2 * (ks & 1) + 1);
+          for (int pg = 0; pg < kPg; ++pg)
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              const int t = 4 * (n >> 1) + (n & 1) + 2 * nt;      // this lane's key
+              const uint8_t* at = kp + pg * kPgBytes;
+              if constexpr (k4) {
+                if (ks == 0) kc[pg][nt] = *reinterpret_cast<const uint4*>(at + 288 * g + 16 * t);
+                const uint32_t w = word_of(kc[pg][nt], ks >> 1), s2 = ksc[pg][nt][ks >> 2];
+                kb[pg][nt][0] = hmul2_u32(e2m1_pick(w, 2 * (ks & 1)), s2);
+                kb[pg][nt][1] = hmul2_u32(e2m1_pick(w, 2 * (ks & 1) + 1), s2);
+              } else {
+                if ((ks & 1) == 0)
+                  kc[pg][nt] = *reinterpret_cast<const uint4*>(at + 288 * t + 64 * g + 16 * ((ks >> 1) ^ (g >> 1)));
+                kb[pg][nt][0] = word_of(kc[pg][nt], 2 * (ks & 1));
+                kb[pg][nt][1] = word_of(kc[pg][nt], 2 * (ks & 1) + 1);
+              }
             }
-          }
 #pragma unroll
           for (int pt = kParts - 1; pt >= 0; --pt) {
             const uint4 a = qs[pt][ks][lane];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) mma16816<k4>(s[nt][pt > 0], a, kb[nt][0], kb[nt][1]);
+            for (int pg = 0; pg < kPg; ++pg)
+#pragma unroll
+              for (int nt = 0; nt < 2; ++nt) mma16816<k4>(s[pg][nt][pt > 0], a, kb[pg][nt][0], kb[pg][nt][1]);
           }
         }
-        // x[h][e]: row n + 8 h, key k0 + 4 g + e
-        float x[2][4];
+        // x[pg][h][e]: row n + 8 h, key k0 + 16 pg + 4 g + e
+        float x[kPg][2][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            x[h][e] = (s[e >> 1][0][2 * h + (e & 1)] + s[e >> 1][1][2 * h + (e & 1)]) * unit[h];
-        uint2 v4[4];                                    // V pieces of this lane's four keys
-        uint4 v16[4][2];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int t = 4 * g + e;
-          if constexpr (k4)
-            v4[e] = *reinterpret_cast<const uint2*>(vp + 288 * (n >> 1) + 16 * t + 8 * (n & 1));
-          else
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              v16[e][c] = *reinterpret_cast<const uint4*>(vp + 272 * t + 16 * (g >> 1) + 32 * n + 16 * c);
-        }
-        // some row of the block does not see some key of the page
-        const bool masked = k0 + 15 > n_past || (k0 < low1 && k0 + 16 > sinks) || passes > 1;
-        if (masked) {
+        for (int pg = 0; pg < kPg; ++pg)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int t = k0 + 4 * g + e;
-              if (!(mine[h] && t <= pos[h] && (t >= plow[h] || t < sinks))) x[h][e] = -INFINITY;
-            }
+            for (int e = 0; e < 4; ++e)
+              x[pg][h][e] = (s[pg][e >> 1][0][2 * h + (e & 1)] + s[pg][e >> 1][1][2 * h + (e & 1)]) * unit[h];
+        uint2 v4[kPg][4];                               // V pieces of this lane's four keys
+        uint4 v16[4][2];
+#pragma unroll
+        for (int pg = 0; pg < kPg; ++pg)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int t = 4 * g + e;
+            const uint8_t* at = vp + pg * kPgBytes;
+            if constexpr (k4)
+              v4[pg][e] = *reinterpret_cast<const uint2*>(at + 288 * (n >> 1) + 16 * t + 8 * (n & 1));
+            else
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                v16[e][c] = *reinterpret_cast<const uint4*>(at + 272 * t + 16 * (g >> 1) + 32 * n + 16 * c);
+          }
+        // some row of the block does not see some key of the pages
+        const bool masked = there != (1u << kPg) - 1u || k0 + 16 * kPg - 1 > n_past || (k0 < low1 && k0 + 16 * kPg > sinks) ||
+                            passes > 1;
+        if (masked) {
+#pragma unroll
+          for (int pg = 0; pg < kPg; ++pg)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int t = k0 + 16 * pg + 4 * g + e;
+                if (!(((there >> pg) & 1u) && mine[h] && t <= pos[h] && (t >= plow[h] || t < sinks))) x[pg][h][e] = -INFINITY;
+              }
           if constexpr (!k4) {
             // V rows that no row sees are zeroed (stale bytes may be anything,
             // and 0 * NaN is NaN); a non-finite element that only some rows see
@@ -361,7 +396,12 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
         }
         float mx[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) mx[h] = fmaxf(fmaxf(x[h][0], x[h][1]), fmaxf(x[h][2], x[h][3]));
+        for (int h = 0; h < 2; ++h) {
+          mx[h] = -INFINITY;
+#pragma unroll
+          for (int pg = 0; pg < kPg; ++pg)
+            mx[h] = fmaxf(mx[h], fmaxf(fmaxf(x[pg][h][0], x[pg][h][1]), fmaxf(x[pg][h][2], x[pg][h][3])));
+        }
         // the reference moves only when a score exceeds it by more than 8
         if (__any_sync(0xffffffffu, mx[0] > ref[0] + 8.f || mx[1] > ref[1] + 8.f)) {
           float a[2];
@@ -384,63 +424,71 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
             o[jj][3] *= a[1];
           }
         }
-        uint4 pa[kParts];
+        uint4 pa[kPg][kParts];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float base = kBias - (ref[h] == -INFINITY ? 0.f : ref[h]);
+        for (int pg = 0; pg < kPg; ++pg) {
+          float (&xp)[2][4] = x[pg];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[h][e] = exp2_approx(x[h][e] + base);
-            lsum[h] += x[h][e];
+          for (int h = 0; h < 2; ++h) {
+            const float base = kBias - (ref[h] == -INFINITY ? 0.f : ref[h]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              xp[h][e] = exp2_approx(xp[h][e] + base);
+              lsum[h] += xp[h][e];
+            }
+          }
+#pragma unroll
+          for (int pt = 0; pt < kParts; ++pt) {
+            pa[pg][pt].x = take_part<k4>(xp[0][0], xp[0][1]);
+            pa[pg][pt].y = take_part<k4>(xp[1][0], xp[1][1]);
+            pa[pg][pt].z = take_part<k4>(xp[0][2], xp[0][3]);
+            pa[pg][pt].w = take_part<k4>(xp[1][2], xp[1][3]);
           }
         }
-#pragma unroll
-        for (int pt = 0; pt < kParts; ++pt) {
-          pa[pt].x = take_part<k4>(x[0][0], x[0][1]);
-          pa[pt].y = take_part<k4>(x[1][0], x[1][1]);
-          pa[pt].z = take_part<k4>(x[0][2], x[0][3]);
-          pa[pt].w = take_part<k4>(x[1][2], x[1][3]);
-        }
         // ------------------------------------------------ O += P . V
-        uint32_t s2[4];
+        uint32_t s2[kPg][4];
         if constexpr (k4) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)                   // scale byte n of keys 4 g + e
-            s2[e] = scale_pair((__shfl_sync(0xffffffffu, vs_word, 2 * (4 * g + e) + (n >> 2)) >> (8 * (n & 3))) & 0xFFu);
+          for (int pg = 0; pg < kPg; ++pg)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)                 // scale byte n of keys 4 g + e
+              s2[pg][e] =
+                  scale_pair((__shfl_sync(0xffffffffu, vs_word[pg], 2 * (4 * g + e) + (n >> 2)) >> (8 * (n & 3))) & 0xFFu);
         }
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {                // d's 16 n + 2i .. 2i + 3: four independent sums
-          uint32_t vb[4][2];
 #pragma unroll
-          for (int ii = 0; ii < 2; ++ii) {
-            uint32_t v[4];
+          for (int pg = 0; pg < kPg; ++pg) {
+            uint32_t vb[4][2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if constexpr (k4)
-                v[e] = hmul2_u32(e2m1_pick(i < 4 ? v4[e].x : v4[e].y, (i & 3) + ii), s2[e]);
-              else
-                v[e] = word_of(v16[e][i >> 2], (i & 3) + ii);
+            for (int ii = 0; ii < 2; ++ii) {
+              uint32_t v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if constexpr (k4)
+                  v[e] = hmul2_u32(e2m1_pick(i < 4 ? v4[pg][e].x : v4[pg][e].y, (i & 3) + ii), s2[pg][e]);
+                else
+                  v[e] = word_of(v16[e][i >> 2], (i & 3) + ii);
+              }
+#pragma unroll
+              for (int hl = 0; hl < 2; ++hl) {
+                const uint32_t sel = hl ? 0x7632u : 0x5410u;
+                vb[2 * ii + hl][0] = __byte_perm(v[0], v[1], sel);
+                vb[2 * ii + hl][1] = __byte_perm(v[2], v[3], sel);
+              }
             }
 #pragma unroll
-            for (int hl = 0; hl < 2; ++hl) {
-              const uint32_t sel = hl ? 0x7632u : 0x5410u;
-              vb[2 * ii + hl][0] = __byte_perm(v[0], v[1], sel);
-              vb[2 * ii + hl][1] = __byte_perm(v[2], v[3], sel);
-            }
+            for (int pt = kParts - 1; pt >= 0; --pt)
+#pragma unroll
+              for (int jj = 0; jj < 4; ++jj) mma16816<k4>(o[2 * i + jj], pa[pg][pt], vb[jj][0], vb[jj][1]);
           }
-#pragma unroll
-          for (int pt = kParts - 1; pt >= 0; --pt)
-#pragma unroll
-            for (int jj = 0; jj < 4; ++jj) mma16816<k4>(o[2 * i + jj], pa[pt], vb[jj][0], vb[jj][1]);
         }
       }
-      // the slot takes page j + kSlots
+      // the slot takes unit j + kSlots
       __syncwarp();
-      have &= ~(1u << b);
-      if (fetch(j + Ring::kSlots, id_next, b)) have |= 1u << b;
-      copy_commit();
+      fetch(j + Ring::kSlots, id_next, b);
       id_next = id_after;
-      id_after = id_of(j + Ring::kSlots + 2);
+      id_after = ids_of(j + Ring::kSlots + 2);
       b = b + 1 == Ring::kSlots ? 0 : b + 1;
     }
     __syncthreads();                                    // the rings are free
@@ -469,17 +517,17 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
     __syncthreads();
     const uint32_t bad = k4 ? 0u : poison;
     const int r_lo = sp.i0 * pl.group, r_hi = min(sp.i1 * pl.group, R);
-    for (int r = r_lo + (tid >> 5); r < r_hi; r += kFewWarps) {        // a warp per row, 4 d's per lane
+    for (int r = r_lo + (tid >> 5); r < r_hi; r += kWarps) {        // a warp per row, 4 d's per lane
       float m = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kFewWarps; ++w) {
+      for (int w = 0; w < kWarps; ++w) {
         const float2 v = ml_sm[w][r];
         if (v.y != 0.f) m = fmaxf(m, v.x);
       }
       float L = 0.f;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kFewWarps; ++w) {
+      for (int w = 0; w < kWarps; ++w) {
         const float2 v = ml_sm[w][r];
         if (v.y == 0.f) continue;                       // the row sees no key of this warp
         const float a = exp2_approx(v.x - m);
@@ -528,7 +576,7 @@ static cudaError_t launch_few(const PattnPlan& pl, const KvView& kv, int layer, 
     if (e != cudaSuccess) return e;
     if (known) have[dev] = true;
   }
-  pattn_few_kernel<k4><<<dim3(pl.slots, pl.nkv), 32 * kFewWarps, FewRing<k4>::kSmem, st>>>(q, pl, kv, layer, part_o, part_ml);
+  pattn_few_kernel<k4><<<dim3(pl.slots, pl.nkv), 32 * FewRing<k4>::kWarps, FewRing<k4>::kSmem, st>>>(q, pl, kv, layer, part_o, part_ml);
   return cudaGetLastError();
 }
 
