@@ -557,7 +557,7 @@ static int check_kv4_rows(spec_ctx* c, const spec_kv* kv, int layer, const float
 int spec_kv4_append(spec_ctx* c, const spec_kv* kv, int layer, const float* k, const float* v, int ld, int n) {
   int rc = check_kv4_rows(c, kv, layer, k, v, ld, n);
   if (rc || n == 0) return rc;
-  return cuda_code(launch_kv4_append(k, v, ld, n, view_of(c, kv), layer, c->status, c->stream));
+  return cuda_code(launch_kv4_append(k, v, ld, n, view_of(c, kv), layer, c->num_sms, c->status, c->stream));
 }
 
 int spec_kv4_read(spec_ctx* c, const spec_kv* kv, int layer, int pos0, int n, float* k, float* v, int ld) {

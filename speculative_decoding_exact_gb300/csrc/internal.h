@@ -125,7 +125,7 @@ cudaError_t launch_qk_norm_rope(const float* x, int ldx, int n, int nq, int nkv,
                                 const QkTransform& t, float* out, int ldo, int32_t* status, cudaStream_t st);
 
 // 4-bit cache (KvView::pool holds 4-bit pages): rows in, rows out
-cudaError_t launch_kv4_append(const float* k, const float* v, int ld, int n, const KvView& kv, int layer,
+cudaError_t launch_kv4_append(const float* k, const float* v, int ld, int n, const KvView& kv, int layer, int num_sms,
                               int32_t* status, cudaStream_t st);
 cudaError_t launch_kv4_read(const KvView& kv, int layer, int pos0, int n, float* k, float* v, int ld,
                             cudaStream_t st);
