@@ -8,6 +8,23 @@
 
 namespace spec {
 
+// Launches a kernel that waits (griddepcontrol.wait) before it touches memory, so
+// that it may start while its predecessor in the stream ends.
+template <class... P, class... A>
+inline cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // ---- launchers (all enqueue on `st`; `pdl` = programmatic dependent launch)
 cudaError_t launch_repack(const void* src, void* dst, int N, int K, cudaStream_t st);
 // withhold: the producer issues no copy (the self-test of the bounded waits:

@@ -175,15 +175,14 @@ cudaError_t launch_kv4_append(const float* k, const float* v, int ld, int n, con
   uint32_t items;
   if (!kv4_items(kv, ((long long)n + 15) / 16 + 1, items)) return cudaErrorInvalidConfiguration;
   const uint32_t most = (uint32_t)(kAppendCtas * num_sms);
-  kv4_append_kernel<<<items < most ? items : most, kKv4Threads, 0, st>>>(k, v, ld, n, items, kv, layer, status);
-  return cudaGetLastError();
+  return launch_early(kv4_append_kernel, dim3(items < most ? items : most), dim3(kKv4Threads), 0, st, k, v, ld, n, items, kv,
+                      layer, status);
 }
 
 cudaError_t launch_kv4_read(const KvView& kv, int layer, int pos0, int n, float* k, float* v, int ld, cudaStream_t st) {
   uint32_t items;
   if (!kv4_items(kv, ((long long)pos0 + n + 15) / 16 - pos0 / 16, items)) return cudaErrorInvalidConfiguration;
-  kv4_read_kernel<<<items, kReadThreads, 0, st>>>(kv, layer, pos0, n, k, v, ld);
-  return cudaGetLastError();
+  return launch_early(kv4_read_kernel, dim3(items), dim3(kReadThreads), 0, st, kv, layer, pos0, n, k, v, ld);
 }
 
 }  // namespace spec

@@ -482,7 +482,7 @@ pattn_merge_kernel(const float4* __restrict__ part_o, const float2* __restrict__
     for (int k = 0; k < kBatch; ++k)
       if (x[k].y != 0.f) top = fmaxf(top, x[k].x);
     if (top > m) {
-      const float a = exp2f(m - top);
+      const float a = exp2_approx(m - top);
       m = top;
       L *= a;
       o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
@@ -490,7 +490,7 @@ pattn_merge_kernel(const float4* __restrict__ part_o, const float2* __restrict__
 #pragma unroll
     for (int k = 0; k < kBatch; ++k)
       if (x[k].y != 0.f) {
-        const float w = exp2f(x[k].x - m);
+        const float w = exp2_approx(x[k].x - m);
         L += w * x[k].y;
         o.x += w * y[k].x;
         o.y += w * y[k].y;
@@ -511,7 +511,7 @@ pattn_merge_kernel(const float4* __restrict__ part_o, const float2* __restrict__
   for (int k = 0; k < kMergeParts; ++k) {
     const float2 x = ml_sm[k][lane];
     if (x.y == 0.f) continue;
-    const float w = exp2f(x.x - m);
+    const float w = exp2_approx(x.x - m);
     const float4 y = o_sm[k][lane];
     L += w * x.y;
     o.x += w * y.x;
@@ -551,9 +551,8 @@ static cudaError_t launch_pattn_kv4(const PattnPlan& pl, const KvView& kv, int l
     if (e != cudaSuccess) return e;
     if (known) have[dev] = true;
   }
-  pattn_kernel<<<dim3(pl.slots, pl.nkv, row_tiles), kPattnThreads, kPattnSmem, st>>>(q, pl, kv, layer, part_o, part_ml,
-                                                                                        status);
-  return cudaGetLastError();
+  return launch_early(pattn_kernel, dim3(pl.slots, pl.nkv, row_tiles), dim3(kPattnThreads), kPattnSmem, st, q, pl, kv, layer,
+                      part_o, part_ml, status);
 }
 
 cudaError_t launch_paged_attention(bool k4, const KvView& kv, int layer, const float* q, int M, int nq, int window,
@@ -588,17 +587,8 @@ cudaError_t launch_paged_attention(bool k4, const KvView& kv, int layer, const f
                   : k4          ? launch_pattn_kv4(pl, kv, layer, q, row_tiles, po, ml, status, st)
                                 : launch_pattn_bf16(pl, kv, layer, q, row_tiles, po, ml, status, st);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(M * nq);
-  cfg.blockDim = dim3(32 * kMergeParts);
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, pattn_merge_kernel, reinterpret_cast<const float4*>(po), (const float2*)ml, pl,
-                            (const int32_t*)kv.seq_len, reinterpret_cast<float4*>(out));
+  return launch_early(pattn_merge_kernel, dim3(M * nq), dim3(32 * kMergeParts), 0, st, reinterpret_cast<const float4*>(po), ml,
+                      pl, kv.seq_len, reinterpret_cast<float4*>(out));
 }
 
 }  // namespace spec

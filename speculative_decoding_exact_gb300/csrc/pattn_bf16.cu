@@ -516,9 +516,8 @@ cudaError_t launch_pattn_bf16(const PattnPlan& pl, const KvView& kv, int layer, 
   CUtensorMap map;
   e = make_kv_tmap(kv, &map);
   if (e != cudaSuccess) return e;
-  pattn_bf16_kernel<<<dim3(pl.slots, pl.nkv, row_tiles), kThreads, kBf16Smem, st>>>(
-      q, pl, kv, map, layer, reinterpret_cast<float4*>(part_o), part_ml, status);
-  return cudaGetLastError();
+  return launch_early(pattn_bf16_kernel, dim3(pl.slots, pl.nkv, row_tiles), dim3(kThreads), kBf16Smem, st, q, pl, kv, map, layer,
+                      reinterpret_cast<float4*>(part_o), part_ml, status);
 }
 
 }  // namespace spec

@@ -576,8 +576,8 @@ static cudaError_t launch_few(const PattnPlan& pl, const KvView& kv, int layer, 
     if (e != cudaSuccess) return e;
     if (known) have[dev] = true;
   }
-  pattn_few_kernel<k4><<<dim3(pl.slots, pl.nkv), 32 * FewRing<k4>::kWarps, FewRing<k4>::kSmem, st>>>(q, pl, kv, layer, part_o, part_ml);
-  return cudaGetLastError();
+  return launch_early(pattn_few_kernel<k4>, dim3(pl.slots, pl.nkv), dim3(32 * FewRing<k4>::kWarps), FewRing<k4>::kSmem, st, q,
+                      pl, kv, layer, part_o, part_ml);
 }
 
 cudaError_t launch_pattn_few(bool k4, const PattnPlan& pl, const KvView& kv, int layer, const float* q, float* part_o,

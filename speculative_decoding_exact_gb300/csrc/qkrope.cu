@@ -89,9 +89,8 @@ cudaError_t launch_qk_norm_rope(const float* x, int ldx, int n, int nq, int nkv,
                                 const QkTransform& t, float* out, int ldo, int32_t* status, cudaStream_t st) {
   const int groups = (nq + kQkHeads - 1) / kQkHeads + (nkv + kQkHeads - 1) / kQkHeads;
   const int warps = groups < kQkWarps ? groups : kQkWarps;
-  qk_norm_rope_kernel<<<dim3(n, (groups + warps - 1) / warps), 32 * warps, 0, st>>>(x, ldx, nq, nkv, pos, t, out, ldo,
-                                                                                  status);
-  return cudaGetLastError();
+  return launch_early(qk_norm_rope_kernel, dim3(n, (groups + warps - 1) / warps), dim3(32 * warps), 0, st, x, ldx, nq, nkv,
+                      pos, t, out, ldo, status);
 }
 
 }  // namespace spec
