@@ -128,8 +128,8 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
     for (int g = 0; g < 4; ++g) gave_up[g] = 0;
     fence_mbarrier_init();
   }
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();                                        // not before: see the merge
   const int n_past = __ldcg(kv.seq_len) - pl.M;
   // the rows of Q, whole rows by a warp, into the last stage (which tile 2 is the
   // first to use), 16-byte chunk j at j ^ (row % 8)
@@ -450,7 +450,8 @@ pattn_merge_kernel(const float4* __restrict__ part_o, const float2* __restrict__
   const int R = pl.M * pl.group, item = blockIdx.x * 32 + lane;       // ((KV head, d / 4), row); a grid of whole warps
   const int hd = div24(item, R), r = item - hd * R, kvh = hd >> 5, d4 = hd & 31;
   const int i = div24(r, pl.group), head = kvh * pl.group + r - i * pl.group;
-  pdl_wait();
+  // The length may be read before the wait: the kernel before this one lets it start
+  // only once its own wait is over, so whatever wrote the length has finished.
   const int n_past = __ldcg(seq_len) - pl.M;
   Span s = span_of(pl, n_past, 0);
   if (i >= s.i1) s = span_of(pl, n_past, 1);
@@ -462,6 +463,7 @@ pattn_merge_kernel(const float4* __restrict__ part_o, const float2* __restrict__
   auto slot = [&](int j) { return j < n0 ? res + kMergeParts * j : c1 + kMergeParts * (j - n0); };
   const size_t step = (size_t)pl.nkv * R, at = (size_t)kvh * R + r;
   const float4* po = part_o + (size_t)hd * R + r;
+  pdl_wait();
   constexpr int kBatch = 8;                             // loads in flight
   float m = -INFINITY, L = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);

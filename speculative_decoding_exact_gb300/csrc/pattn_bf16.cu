@@ -100,8 +100,8 @@ pattn_bf16_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, const __
     for (int g = 0; g < 4; ++g) gave_up[g] = 0;
     fence_mbarrier_init();
   }
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();                                        // not before: see the merge in pattn.cu
   const int n_past = __ldcg(kv.seq_len) - pl.M;
   // Q, whole rows by a warp, as swizzled K-major tiles: [part][d half][row][128 B]
   const int qw = warp < kWLoadK ? warp : warp - 2;

@@ -119,8 +119,8 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
   if (tid < kFewRows) qmax[tid] = 0;
   if (tid == 32) poison = 0;
   uint8_t* ring = sm + warp * Ring::kWarp;
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();                                        // not before: see the merge in pattn.cu
   const int n_past = __ldcg(kv.seq_len) - pl.M;
   // this thread's rows n and n + 8; in the first 8 warps the Q elements of MMA
   // `warp` (bf16: the 16-byte pieces of a K row in an order that depends on g)
