@@ -12,14 +12,15 @@
 // it fills by cp.async (16 bytes per lane; bulk copies to padded places are issued
 // lane by lane and cost 150 instructions a page).
 //
-// What bounds it: the dependent steps of a few warps.  A 4-bit page is 491 warp
+// What bounds it: the dependent steps of a few warps.  A 4-bit page is 520 warp
 // instructions, 64 of them MMAs of 8 cycles; two warps per scheduler fill 42 % of the
 // slots, 2,300 cycles a tile against 800 at the SM's share of HBM.  One token of 52
-// heads on 4 behind 128k keys: 41 us in 4 bits (one page at a time, 12 warps: 43, 596
-// instructions a page), 59 in bf16 (12 warps, 168 registers each); 10.3 us behind 2k
-// keys, of which the second launch is 4.  (Pages loaded into registers in fragment
-// order: 52.  Keys on the 128 rows of tcgen05 MMAs and query rows as columns: 42,
-// with twice the code.)
+// heads on 4 behind 128k keys: 41 us in 4 bits, 61 in bf16; 8.1 us behind 2k keys, of
+// which the join is 3.  (12 warps of 168 registers: 40 and 60 us, but 8.7 behind 2k
+// keys, and 10.4 instead of 9.4 for a bf16 window of 1024.  One 4-bit page at a time:
+// 5 % slower.  Pages loaded into registers in fragment order: 52 when this took 43.
+// Keys on the 128 rows of tcgen05 MMAs and query rows as columns: 42, with twice the
+// code.)
 //
 // The d's of a K row and the d's and keys of a V page may be visited in any
 // order.  Lane 4n + g (g < 4) takes d's 32 g .. of K (one 16-byte chunk of codes, 64
@@ -32,7 +33,9 @@
 //
 // Precision: as pattn.cu for the 4-bit cache (binary16, q and p in two parts,
 // row-wise powers of two).  bf16 pages are operands as they are, with q and p in
-// three bf16 parts (24 significant bits): no value is out of range.
+// three bf16 parts (24 significant bits): no value is out of range.  A unit's O is
+// added up in fp32, since the MMAs truncate: left in their accumulators over the 27
+// pages of a warp it was off by 1.2e-6 instead of 4e-7 (and 2.5 us faster).
 #include "attn_mma.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -41,6 +44,7 @@
 
 namespace spec {
 
+constexpr int kFewWarps = 8;
 constexpr int kOPitch = 132;               // floats between rows of a warp's O in shared memory
 // A warp's ring of pages in shared memory.  Where a piece of 16 bytes lies keeps
 // the eight lanes of a load phase in different banks:
@@ -48,11 +52,11 @@ constexpr int kOPitch = 132;               // floats between rows of a warp's O 
 //   bf16:  K row t at 288 t, V row t at 272 t + 16 (t / 8)
 template <bool k4>
 struct FewRing {
-  static constexpr int kWarps = k4 ? 8 : 12, kPg = k4 ? 2 : 1;      // kPg: pages of a unit
+  static constexpr int kPg = k4 ? 2 : 1;                // pages of a unit
   static constexpr int kK = k4 ? 4 * 288 + 128 : 16 * 288, kV = k4 ? kK : 16 * 272 + 16;
-  static constexpr int kSlots = k4 ? 3 : 2;
-  static constexpr int kWarp = kSlots * kPg * (kK + kV), kO = 4 * kWarps * kFewRows * kOPitch;
-  static constexpr size_t kSmem = kWarps * kWarp > kO ? kWarps * kWarp : kO;
+  static constexpr int kSlots = 3;
+  static constexpr int kWarp = kSlots * kPg * (kK + kV), kO = 4 * kFewWarps * kFewRows * kOPitch;
+  static constexpr size_t kSmem = kFewWarps * kWarp > kO ? kFewWarps * kWarp : kO;
 };
 template <bool k4>
 SPEC_DEV void mma16816(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
@@ -64,6 +68,18 @@ SPEC_DEV void mma16816(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) 
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+// the same onto zero
+template <bool k4>
+SPEC_DEV void mma16816_first(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  if constexpr (k4)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
 }
 // the operand part of a pair (x0 in the low half); x becomes what is left
 template <bool k4>
@@ -99,14 +115,14 @@ SPEC_DEV uint32_t e2m1_pick(uint32_t w, int b) {        // b known at compile ti
 SPEC_DEV uint32_t scale_pair(uint32_t byte) { return byte * 0x00800080u; }
 
 template <bool k4>
-__global__ void __launch_bounds__(32 * FewRing<k4>::kWarps, 1)
+__global__ void __launch_bounds__(32 * kFewWarps, 1)
 pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, float* __restrict__ part_o,
                  float2* __restrict__ part_ml) {
   constexpr int kParts = k4 ? 2 : 3;                    // of q and p
   constexpr float kBias = k4 ? 7.f : 0.f;               // p = 2^(bias + s - max)
   constexpr int kPageBytes = k4 ? kKv4PageBytes : 4096;
   using Ring = FewRing<k4>;
-  constexpr int kWarps = Ring::kWarps, kPg = Ring::kPg, kUnitsPerTile = kPagesPerTile / kPg;
+  constexpr int kWarps = kFewWarps, kPg = Ring::kPg, kUnitsPerTile = kPagesPerTile / kPg;
   extern __shared__ __align__(128) uint8_t sm[];
   float* o_sm = reinterpret_cast<float*>(sm);           // [warp][row][kOPitch], where the rings were
   __shared__ uint4 qs[kParts][8][32];                   // A fragments
@@ -457,6 +473,7 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
         }
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {                // d's 16 n + 2i .. 2i + 3: four independent sums
+          float oi[4][4];                               // of this unit
 #pragma unroll
           for (int pg = 0; pg < kPg; ++pg) {
             uint32_t vb[4][2];
@@ -480,8 +497,17 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
 #pragma unroll
             for (int pt = kParts - 1; pt >= 0; --pt)
 #pragma unroll
-              for (int jj = 0; jj < 4; ++jj) mma16816<k4>(o[2 * i + jj], pa[pg][pt], vb[jj][0], vb[jj][1]);
+              for (int jj = 0; jj < 4; ++jj) {
+                if (pg == 0 && pt == kParts - 1)
+                  mma16816_first<k4>(oi[jj], pa[pg][pt], vb[jj][0], vb[jj][1]);
+                else
+                  mma16816<k4>(oi[jj], pa[pg][pt], vb[jj][0], vb[jj][1]);
+              }
           }
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[2 * i + jj][c] += oi[jj][c];
         }
       }
       // the slot takes unit j + kSlots
@@ -576,7 +602,7 @@ static cudaError_t launch_few(const PattnPlan& pl, const KvView& kv, int layer, 
     if (e != cudaSuccess) return e;
     if (known) have[dev] = true;
   }
-  return launch_early(pattn_few_kernel<k4>, dim3(pl.slots, pl.nkv), dim3(32 * FewRing<k4>::kWarps), FewRing<k4>::kSmem, st, q,
+  return launch_early(pattn_few_kernel<k4>, dim3(pl.slots, pl.nkv), dim3(32 * kFewWarps), FewRing<k4>::kSmem, st, q,
                       pl, kv, layer, part_o, part_ml);
 }
 
