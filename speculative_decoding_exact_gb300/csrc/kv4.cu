@@ -4,10 +4,10 @@
 // Both kernels make one pass over their data: 4 bytes per value on the fp32
 // side and 9/16 on the paged side, so they are bound by memory traffic.  A CTA
 // takes the 16 positions of one page and KV head, K and V, so that the pages are
-// written and read whole.  32761 rows of 4 KV heads: 27 us to append (134 MB read)
-// and 28 to read back (134 MB written), 5.5 TB/s.  Appending with a CTA per item
-// instead of a loop that loads ahead took 30; reading back in such a loop, or with
-// 256 threads instead of 128, 31 and 29.
+// written and read whole.  32761 rows of 4 KV heads: 48 us to append (134 MB read)
+// and read back (134 MB written), 6.4 TB/s; alone 27 and 28.  Appending with a CTA
+// per item instead of a loop that loads ahead took 30; reading back in such a loop,
+// or with 256 threads instead of 128, 31 and 29.
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.cuh"

@@ -31,10 +31,10 @@
 //
 // What bounds it: 32 MMAs of 128 x 128 x 16 take 2,600 cycles a tile, the softmax
 // and the unpacking 8,400 warp instructions (2,100 cycles of four schedulers at
-// best, 47 % of the slots are used): 3,200 cycles a tile.  A call of one tile per
+// best, half of the slots are used): 3,200 cycles a tile.  A call of one tile per
 // CTA is latency: 3,000 cycles to the sequence length and the plan, 4,700 to page
 // ids, pages and the unpacked K, 3,900 for the tile, 2,500 to store.  16 rows of 52
-// heads on 4: 14.4 us behind 2k keys, 37.7 behind 32k (370 TFLOP/s, counting each
+// heads on 4: 11.5 us behind 2k keys, 34.2 behind 32k (408 TFLOP/s, counting each
 // product once; two parts make it two).
 //
 // Precision: all operands are binary16.  A 4-bit value is exact in it; q and p are
@@ -527,7 +527,7 @@ pattn_merge_kernel(const float4* __restrict__ part_o, const float2* __restrict__
 
 // chunks of a KV head at most: one per SM, KV head and row tile, so that the
 // grid is one wave.  (With as many for two row tiles, two waves, 16 rows of 13
-// heads take 57 instead of 45 us behind 32k keys.)  At least 4, so that
+// heads took 57 instead of 45 us behind 32k keys.)  At least 4, so that
 // a window's chunks (one of sinks, and one more than the window's own) fit.
 static int pattn_chunks(int nkv, int row_tiles, int num_sms) {
   const int c = num_sms / (nkv * row_tiles);

@@ -9,13 +9,13 @@
 // thread touches K.  Q and P go in three bf16 parts by truncation, 24 bits, so
 // nothing is rounded and no value is out of range.  Binary16 operands (two parts)
 // took conversions of every page and a second path for elements past binary16;
-// 104 rows over 32k keys took 48 us with them, 39 with this.
+// 104 rows over 32k keys took 48 us with them when this took 39 (now 35).
 //
 // What bounds it: the MMAs.  A 128 x 128 x 16 product takes 121 cycles with both
 // operands in shared memory (Q . K^T) and 81 with one in TMEM (P . V), 48 of them
 // 4,850 cycles a tile; the tile's 64 KB come in 2,850 at the SM's share of HBM.  The
 // TMEM has no room for more than one of Q's parts beside S, P and O.  16 rows of 52
-// heads on 4 with a window of 4096: 20.5 us, most of it latency of two tiles.
+// heads on 4 with a window of 4096: 16.4 us, most of it latency of two tiles.
 //
 // 0 * NaN is NaN, so an element of V that is not finite would reach rows that do
 // not see its key.  Four warps look through each V tile before its MMAs; such
