@@ -430,7 +430,8 @@ SPEC_API int spec_attention(spec_ctx* ctx, const spec_kv* kv, int layer,
  * every call of a kind that places it at the same position, and differs by
  * rounding between kinds (a token alone and inside a verify block, say).  A
  * layer that is a sliding-window layer of the ctx keeps its K/V in a ring, not
- * in the pool, and is refused (SPEC_EINVAL).
+ * in the pool, and is refused (SPEC_EINVAL).  A bounded device wait that gives
+ * up sets SPEC_ST_DEVICE_WAIT in the ctx status word, and out is incomplete.
  * q DEVICE fp32 [M][n_q_heads][head_dim]; out DEVICE fp32
  * [M][n_q_heads*head_dim]; both 16-byte aligned, not overlapping. */
 SPEC_API int spec_attention_window(spec_ctx* ctx, const spec_kv* kv, int layer, const float* q, int M,

@@ -101,9 +101,9 @@ def attend(ctx, kv, kind, q, window, sinks, layer=1):
     return out.cpu().numpy()
 
 
-# what q, p and the values lose as MMA operands (kv4_util): two binary16 parts,
-# and for bf16 values below 2^-17, of which these inputs have some, 2^-25 each
-SPLIT = {"kv4": 2.0 ** -22, "bf16": 2.0 ** -21}
+# what q and p lose as MMA operands (kv4_util): two binary16 parts against 4-bit
+# values, three bf16 parts, 24 bits, against bf16 ones
+SPLIT = {"kv4": 2.0 ** -22, "bf16": 2.0 ** -24}
 
 
 def check_attention(ctx, kind, M, length, window, sinks, seed=0, spread=1.0, q_scale=1.0):
@@ -403,8 +403,8 @@ def test_attention_is_untouched_by_what_rows_do_not_see(kind, window, sinks, nq)
 @pytest.mark.parametrize("nq", [26, 2])
 @pytest.mark.parametrize("M,window,sinks", [(1, 0, 0), (16, 0, 0), (16, 100, 5), (5, 40, 200)])
 def test_attention_bf16_values_past_binary16(M, window, sinks, nq):
-    """bf16 elements from 2^15 up to the type's largest, and whole tiny rows:
-    what binary16 operands cannot hold is worked on in fp32."""
+    """bf16 elements from 2^15 up to the type's largest, and whole tiny rows, which
+    binary16 operands could not hold."""
     ctx = context(nq, 2)
     length = 400
     kv, k, v, ids = cache(ctx, "bf16", length, 71)
