@@ -40,7 +40,7 @@ SPEC_DEV uint8_t* kv4_page(const KvView& kv, int page, int layer, int head) {
 // A CTA works on every gridDim.x-th item, (tile, head), and loads the next one's
 // rows before it quantises this one's.
 __global__ void __launch_bounds__(kKv4Threads, kAppendCtas)
-kv4_append_kernel(const float* __restrict__ k, const float* __restrict__ v, long long ld, int n, uint32_t items, KvView kv,
+kv4_append_kernel(const float* k, const float* v, long long ld, int n, uint32_t items, KvView kv,
                   int layer, int32_t* status) {
   pdl_trigger();
   const int sub = threadIdx.x & 15, t = threadIdx.x >> 4;

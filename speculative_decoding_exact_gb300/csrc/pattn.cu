@@ -130,7 +130,7 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
   }
   pdl_wait();
   pdl_trigger();                                        // not before: see the merge
-  const int n_past = __ldcg(kv.seq_len) - pl.M;
+  const int n_past = ldg_now(kv.seq_len) - pl.M;
   // the rows of Q, whole rows by a warp, into the last stage (which tile 2 is the
   // first to use), 16-byte chunk j at j ^ (row % 8)
   uint8_t* q_rows = sm + (kStages - 1) * kStageBytes;
@@ -452,7 +452,7 @@ pattn_merge_kernel(const float4* __restrict__ part_o, const float2* __restrict__
   const int i = div24(r, pl.group), head = kvh * pl.group + r - i * pl.group;
   // The length may be read before the wait: the kernel before this one lets it start
   // only once its own wait is over, so whatever wrote the length has finished.
-  const int n_past = __ldcg(seq_len) - pl.M;
+  const int n_past = ldg_now(seq_len) - pl.M;
   Span s = span_of(pl, n_past, 0);
   if (i >= s.i1) s = span_of(pl, n_past, 1);
   const int slots = n_past + i < 0 ? 0 : min(s.nslots, pl.slots);
@@ -476,8 +476,8 @@ pattn_merge_kernel(const float4* __restrict__ part_o, const float2* __restrict__
       x[k] = make_float2(0.f, 0.f);
       if (j0 + k < n) {
         const size_t c = slot(j0 + k);
-        x[k] = __ldcg(part_ml + at + c * step);
-        y[k] = __ldcg(po + 32 * c * step);
+        x[k] = ldg_now(part_ml + at + c * step);
+        y[k] = ldg_now(po + 32 * c * step);
       }
     }
 #pragma unroll

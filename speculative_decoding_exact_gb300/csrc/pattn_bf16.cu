@@ -102,7 +102,7 @@ pattn_bf16_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, const __
   }
   pdl_wait();
   pdl_trigger();                                        // not before: see the merge in pattn.cu
-  const int n_past = __ldcg(kv.seq_len) - pl.M;
+  const int n_past = ldg_now(kv.seq_len) - pl.M;
   // Q, whole rows by a warp, as swizzled K-major tiles: [part][d half][row][128 B]
   const int qw = warp < kWLoadK ? warp : warp - 2;
   float4 y[kQRows];
@@ -113,7 +113,7 @@ pattn_bf16_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, const __
     for (int j = 0; j < kQRows; ++j) {
       y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (kQRows * qw + j < nr)
-        y[j] = reinterpret_cast<const float4*>(q + ((size_t)i * pl.nq + kvh * pl.group + hd) * 128)[lane];
+        y[j] = ldg_now(reinterpret_cast<const float4*>(q + ((size_t)i * pl.nq + kvh * pl.group + hd) * 128) + lane);
       if (++hd == pl.group) {
         hd = 0;
         ++i;

@@ -141,7 +141,7 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
   uint8_t* ring = sm + warp * Ring::kWarp;
   pdl_wait();
   pdl_trigger();                                        // not before: see the merge in pattn.cu
-  const int n_past = __ldcg(kv.seq_len) - pl.M;
+  const int n_past = ldg_now(kv.seq_len) - pl.M;
   // this thread's rows n and n + 8; in the first 8 warps the Q elements of MMA
   // `warp` (bf16: the 16-byte pieces of a K row in an order that depends on g)
   const int q_at = k4 ? 32 * g + 4 * warp : 32 * g + 8 * ((warp >> 1) ^ (g >> 1)) + 4 * (warp & 1);
@@ -155,8 +155,8 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
     plow[h] = window_low(pl, pos[h]);
     qv[h] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < R && warp < 8)
-      qv[h] = *reinterpret_cast<const float4*>(
-          q + ((size_t)row_i[h] * pl.nq + kvh * pl.group + r - row_i[h] * pl.group) * 128 + q_at);
+      qv[h] = ldg_now(reinterpret_cast<const float4*>(
+          q + ((size_t)row_i[h] * pl.nq + kvh * pl.group + r - row_i[h] * pl.group) * 128 + q_at));
   }
   const int passes = span_count(pl, n_past);
   TileList tl0 = tiles_of(span_of(pl, n_past, 0), slot), tl1;

@@ -21,7 +21,7 @@ constexpr int kQkHeads = 8;                // heads of a warp
 constexpr int kQkWarps = 8;                // warps of a CTA at most
 
 __global__ void __launch_bounds__(32 * kQkWarps)
-qk_norm_rope_kernel(const float* x, long long ldx, int nq, int nkv, const int32_t* __restrict__ pos, QkTransform t,
+qk_norm_rope_kernel(const float* x, long long ldx, int nq, int nkv, const int32_t* pos, QkTransform t,
                     float* out, long long ldo, int32_t* status) {
   pdl_trigger();
   const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15, row = blockIdx.x;
