@@ -768,3 +768,54 @@ def test_two_contexts_on_two_streams():
         assert status(ctx) == 0
     for ctx in {id(j[0]): j[0] for j in jobs}.values():
         ctx.close()
+
+
+@pytest.mark.parametrize("nq,M", [(2, 3), (26, 9)])
+def test_calls_back_to_back_see_what_the_call_before_wrote(nq, M):
+    """Reading, appending over the same positions, norm and rotation of q, attention,
+    again and again without a pause (each kernel may start while the one before
+    ends): the same bits as with a pause after every call."""
+    ctx = context(nq, 2, max_ctx=1024, rope_theta=1e4)
+    rounds, n, length = 24, 200, 700
+    kv, _, _, _ = cache(ctx, "kv4", length, 5)
+    start = kv.pool.clone()
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    rows = torch.randn(rounds, n, 512, generator=gen, device="cuda")
+    x = torch.randn(rounds, M, (nq + 2) * 128, generator=gen, device="cuda")
+    pos = torch.arange(length - M, length, dtype=torch.int32, device="cuda")
+    table = kv.page_table.clone()
+    other = torch.flip(table[:length // 16].clone(), (0,))
+    st = kv.struct()
+
+    def run(pause):
+        kv.pool.copy_(start)
+        held = torch.empty(rounds, n, 512, device="cuda")
+        qk = torch.empty_like(x)
+        q = torch.empty(rounds, M, nq * 128, device="cuda")
+        out = torch.empty(rounds, M, nq * 128, device="cuda")
+        sync()
+        rest = sync if pause else (lambda: None)
+        for i in range(rounds):
+            # the pages change places every other round
+            kv.page_table[:length // 16].copy_(other if i % 2 else table[:length // 16])
+            rest()
+            r, h = rows[i].data_ptr(), held[i].data_ptr()
+            abi.check("read", abi.spec_kv4_read(ctx.h, st, 1, length - n, n, h, h + 1024, 512))
+            rest()
+            abi.check("append", abi.spec_kv4_append(ctx.h, st, 1, r, r + 1024, 512, n))
+            rest()
+            abi.check("qk", abi.spec_qk_norm_rope(ctx.h, x[i].data_ptr(), x.shape[2], M, pos.data_ptr(), None, None,
+                                                  qk[i].data_ptr(), x.shape[2]))
+            rest()
+            q[i].copy_(qk[i, :, :nq * 128])
+            rest()
+            abi.check("attention", abi.spec_attention_kv4(ctx.h, st, 1, q[i].data_ptr(), M, 300, 7, out[i].data_ptr()))
+            rest()
+        sync()
+        return held, out
+    want = run(True)
+    for _ in range(3):
+        got = run(False)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    kv.page_table.copy_(table)
+    assert status(ctx) == 0
