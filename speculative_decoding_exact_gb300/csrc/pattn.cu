@@ -435,8 +435,10 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
 // mod 4; a warp takes 32 neighbouring rows, which lie side by side in the
 // partials.  With m the largest chunk maximum (base 2) and w_c = 2^(m_c - m):
 //   out = sum_c w_c o_c / sum_c w_c l_c, over the chunks in which the row sees a
-// key, first within each residue in chunk order, then over the residues, so the
-// order does not depend on the block.
+// key, first within each residue in chunk order with a running maximum, then over
+// the residues.  Every step is one of the row's own chunks, so a row's bits do not
+// depend on the block.  (Rescaled once per batch of 8 loads the bits did, where the
+// first row's window started in an earlier chunk.)
 // ---------------------------------------------------------------------------
 constexpr int kMergeParts = 4;
 
@@ -470,7 +472,6 @@ pattn_merge_kernel(const float4* __restrict__ part_o, const float2* __restrict__
   for (int j0 = 0; j0 < n; j0 += kBatch) {
     float4 y[kBatch];
     float2 x[kBatch];
-    float top = m;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       x[k] = make_float2(0.f, 0.f);
@@ -480,24 +481,19 @@ pattn_merge_kernel(const float4* __restrict__ part_o, const float2* __restrict__
         y[k] = ldg_now(po + 32 * c * step);
       }
     }
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k)
-      if (x[k].y != 0.f) top = fmaxf(top, x[k].x);
-    if (top > m) {
-      const float a = exp2_approx(m - top);
-      m = top;
-      L *= a;
-      o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
-    }
+    // one chunk after the other, in rounded operations that are spelled out: what
+    // depended on the place in the batch would depend on where the block's list starts
 #pragma unroll
     for (int k = 0; k < kBatch; ++k)
       if (x[k].y != 0.f) {
-        const float w = exp2_approx(x[k].x - m);
-        L += w * x[k].y;
-        o.x += w * y[k].x;
-        o.y += w * y[k].y;
-        o.z += w * y[k].z;
-        o.w += w * y[k].w;
+        const float up = x[k].x - m, e = exp2_approx(-fabsf(up));      // m = -inf at first: 0
+        const float a = up > 0.f ? e : 1.f, w = up > 0.f ? 1.f : e;
+        m = fmaxf(m, x[k].x);
+        L = fmaf(w, x[k].y, __fmul_rn(L, a));
+        o.x = fmaf(w, y[k].x, __fmul_rn(o.x, a));
+        o.y = fmaf(w, y[k].y, __fmul_rn(o.y, a));
+        o.z = fmaf(w, y[k].z, __fmul_rn(o.z, a));
+        o.w = fmaf(w, y[k].w, __fmul_rn(o.w, a));
       }
   }
   o_sm[res][lane] = o;
