@@ -250,11 +250,12 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    // log2(e) / sqrt(d) times the row's power of two: scores in base-2 units
-    float unit = 1.4426950408889634f / sqrtf(128.0f);
+    // what turns scores into base-2 units: a power of two, so that its products are
+    // exact and the largest score less itself is 0 however large it is
+    float unit;
     {
-      // the row is scaled by a power of two to at most 2 in magnitude, and the
-      // scores are scaled back
+      // the row times log2(e) / sqrt(d), by a power of two to about 2 in magnitude at
+      // most, and the scores are scaled back
       float4 y[16];
       float mx = 0.f;
 #pragma unroll
@@ -267,8 +268,8 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
       named_bar(1 + ww, 64);
       mx = fmaxf(mx, pair[1 - h][r]);
       const int e = min(max((int)((__float_as_uint(mx) >> 23) & 255u) - 127, -100), 100);
-      const float mul = __uint_as_float((uint32_t)(127 - e) << 23);
-      unit *= __uint_as_float((uint32_t)(127 + e) << 23);
+      const float mul = 8.f * kScoreScale * __uint_as_float((uint32_t)(127 - e) << 23);
+      unit = __uint_as_float((uint32_t)(124 + e) << 23);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t hi[16], lo[16];
@@ -350,18 +351,19 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
           m4[e & 3] = fmaxf(m4[e & 3], fmaxf(a, b));
         }
         float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * unit;
-        // The reference moves only when a score exceeds it by more than 8 (p
-        // would exceed 2^15).  A wait that ran out is carried to this barrier,
-        // where the pair of warps leaves together.
+        // The reference moves only when a score exceeds it by more than 7: p stays
+        // within 2^15 with the bias, which rounds to at most 8 beside large scores.
+        // A wait that ran out is carried to this barrier, where the pair of warps
+        // leaves together.
         if (!got || !ok) *reinterpret_cast<volatile int*>(&gave_up[ww]) = 1;
-        if (named_bar_or(1 + ww, 64, mx > ref + 8.f || !got || !ok)) {
+        if (named_bar_or(1 + ww, 64, mx - ref > 7.f || !got || !ok)) {
           left = *reinterpret_cast<volatile int*>(&gave_up[ww]) != 0;
           if (left) break;
           pair[h][r] = mx;
           named_bar(1 + ww, 64);
           mx = fmaxf(mx, pair[1 - h][r]);
           if (pending) ok = drain();                    // O so far is in the old units
-          if (mx > ref + 8.f) {
+          if (mx - ref > 7.f) {
             const float a = ref == -INFINITY ? 1.f : exp2_approx(ref - mx);
             ref = mx;
             lsum *= a;

@@ -163,6 +163,9 @@ pattn_bf16_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, const __
       const int r = kQRows * qw + j;
       if (r >= 32 * row_warps) break;
       uint8_t* dst = sm + (lane >> 4) * kHalf + r * 128 + ((((lane & 15) >> 1) ^ (r & 7)) << 4) + 8 * (lane & 1);
+      // log2(e) / sqrt(d) goes into Q: the scores come in base-2 units, and the largest
+      // less itself is 0 however large it is
+      y[j] = make_float4(y[j].x * kScoreScale, y[j].y * kScoreScale, y[j].z * kScoreScale, y[j].w * kScoreScale);
 #pragma unroll
       for (int pt = 0; pt < kParts; ++pt) {
         uint2 w;
@@ -320,7 +323,6 @@ pattn_bf16_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, const __
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    const float unit = 1.4426950408889634f / sqrtf(128.0f);   // scores in base-2 units
     const int p = n_past + i, plow = window_low(pl, p);
     bool ok = true, left = false;
     int it = 0;
@@ -384,12 +386,13 @@ pattn_bf16_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, const __
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int e = 0; e < 64; ++e) m4[e & 3] = fmaxf(m4[e & 3], x[e]);
-        float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * unit;
-        // The reference moves only when a score exceeds it by more than 8.  A wait
+        float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        // The reference moves only when a score exceeds it by more than 8 (a
+        // difference, which is exact for large scores too).  A wait
         // that ran out is carried to this barrier, where the pair of warps leaves
         // together.
         if (!ok) *reinterpret_cast<volatile int*>(&gave_up[ww]) = 1;
-        if (named_bar_or(1 + ww, 64, mx > ref + 8.f || !ok)) {
+        if (named_bar_or(1 + ww, 64, mx - ref > 8.f || !ok)) {
           left = *reinterpret_cast<volatile int*>(&gave_up[ww]) != 0;
           if (left) break;
           pair[h][r] = mx;
@@ -399,7 +402,7 @@ pattn_bf16_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, const __
             ok = pv_wait();
             if (ok) drain();
           }
-          if (mx > ref + 8.f) {
+          if (mx - ref > 8.f) {
             const float a = ref == -INFINITY ? 1.f : exp2_approx(ref - mx);
             ref = mx;
             lsum *= a;
@@ -418,8 +421,8 @@ pattn_bf16_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, const __
           for (int e = 0; e < 8; ++e) {
             float& a = x[16 * c + 2 * e];
             float& b = x[16 * c + 2 * e + 1];
-            a = exp2_approx(fmaf(a, unit, base));
-            b = exp2_approx(fmaf(b, unit, base));
+            a = exp2_approx(a + base);
+            b = exp2_approx(b + base);
             sum += a + b;
             float a1 = a, b1 = b;
 #pragma unroll

@@ -123,7 +123,9 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
 pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, float* __restrict__ part_o,
                  float2* __restrict__ part_ml) {
   constexpr int kParts = k4 ? 2 : 3;                    // of q and p
-  constexpr float kBias = k4 ? 7.f : 0.f;               // p = 2^(bias + s - max)
+  // p = 2^(bias + s - max), s - max at most the lag: 2^15 in binary16, where the bias
+  // rounds to at most 8 beside large scores
+  constexpr float kBias = k4 ? 7.f : 0.f, kLag = k4 ? 7.f : 8.f;
   constexpr int kPageBytes = k4 ? kKv4PageBytes : 4096;
   using Ring = FewRing<k4>;
   constexpr int kWarps = kFewWarps, kPg = Ring::kPg, kUnitsPerTile = kPagesPerTile / kPg;
@@ -422,15 +424,16 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
           for (int pg = 0; pg < kPg; ++pg)
             mx[h] = fmaxf(mx[h], fmaxf(fmaxf(x[pg][h][0], x[pg][h][1]), fmaxf(x[pg][h][2], x[pg][h][3])));
         }
-        // the reference moves only when a score exceeds it by more than 8
-        if (__any_sync(0xffffffffu, mx[0] > ref[0] + 8.f || mx[1] > ref[1] + 8.f)) {
+        // the reference moves only when a score exceeds it by more than kLag (a
+        // difference, which is exact for large scores too)
+        if (__any_sync(0xffffffffu, mx[0] - ref[0] > kLag || mx[1] - ref[1] > kLag)) {
           float a[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
             a[h] = 1.f;
-            if (mx[h] > ref[h] + 8.f) {
+            if (mx[h] - ref[h] > kLag) {
               if (ref[h] != -INFINITY) a[h] = exp2_approx(ref[h] - mx[h]);
               ref[h] = mx[h];
             }

@@ -8,6 +8,7 @@ namespace spec {
 
 constexpr int kKeys = 128;                          // keys of a tile
 constexpr int kPagesPerTile = kKeys / 16;
+constexpr float kScoreScale = (float)(1.4426950408889634 / 11.313708498984761);   // log2(e) / sqrt(128)
 
 struct PattnPlan {
   int M, nq, nkv, group, window, sinks;

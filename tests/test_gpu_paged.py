@@ -68,3 +68,81 @@ def test_a_window_that_starts_in_another_chunk_leaves_a_rows_bits(kind, case):
         part = attend(ctx, kv, kind, q[i:i + m], window, sinks)
         assert same_bits(part, whole[i:i + m]), (i, m)
     assert status(ctx) == 0
+
+
+# ---------------------------------------------------------------------------
+# scores far past a softmax's usual range
+# ---------------------------------------------------------------------------
+def one_hot(q, k, v, nq, length):
+    """Rows' V of the key with the largest score (causal), and which rows have one."""
+    M, nkv = q.shape[0], k.shape[1]
+    o, sure = np.zeros((M, nq, 128)), np.zeros((M, nq), dtype=bool)
+    for h in range(nq):
+        at = h // (nq // nkv)
+        kh, vh, qh = k[:length, at], v[:length, at], q[:, h].astype(np.float64)
+        s, size = kh @ qh.T, np.abs(kh) @ np.abs(qh).T                    # [length][M]
+        for i in range(M):
+            n = length - M + i + 1
+            top = s[:n, i].argmax()
+            rest = np.delete(s[:n, i], top)
+            # split, 256 products' sums and the scaling (kv4_util), and 2^8 in base 2
+            lead = (s[top, i] - rest.max()) if n > 1 else np.inf
+            o[i, h] = vh[top]
+            sure[i, h] = lead > 4 * 520 * EPS * size[:n, i].max() + 2.0 ** 12
+    return o, sure
+
+
+@pytest.mark.parametrize("nq,M", [(2, 3), (26, 3), (26, 16)])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("q_exp,k_exp", [(8, 8), (16, 12), (20, 12), (24, 12), (40, 12), (98, 0), (110, 0)])
+def test_scores_of_any_size_that_fp32_holds(kind, q_exp, k_exp, nq, M):
+    check_one_hot(kind, 2.0 ** q_exp, 2.0 ** k_exp, nq, M)
+
+
+def check_one_hot(kind, q_scale, spread, nq, M):
+    ctx = context(nq, 2)
+    length = 700
+    kv, k, v, _ = cache(ctx, kind, length, 17, spread=spread)
+    q = (np.random.default_rng(3).standard_normal((M, nq, 128)) * q_scale).astype(np.float32)
+    assert np.isfinite(q).all()
+    got = attend(ctx, kv, kind, q, 0, 0).reshape(M, nq, 128)
+    want, sure = one_hot(q, k, v, nq, length)
+    assert sure.mean() > 0.8
+    assert np.isfinite(got[sure]).all()
+    assert (np.abs(got - want)[sure] <= 4 * EPS * np.abs(want[sure])).all()
+    assert status(ctx) == 0
+
+
+@pytest.mark.parametrize("nq,M", [(64, 3), (128, 9)])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("exponent", [23, 25, 26, 27, 30])
+def test_large_scores_that_rise_a_little(kind, exponent, nq, M):
+    """The largest score of a chunk's later tiles lies a little above that of its first
+    ones, both near 2^exponent, where fp32 scores are that far apart: finite, and
+    between V's smallest and largest values.  (64 KV heads: four chunks of four tiles.)"""
+    ctx = context(nq, 64)
+    length = 2048
+    kv, k, v, ids = cache(ctx, kind, length, 19)
+    for rise in (7.0, 8.0, 9.0, 12.0, 15.0, 16.0, 17.0):
+        rows = np.zeros((length, 64, 128), dtype=np.float32)
+        rows[:, :, 0] = 48.0
+        rows[np.arange(length) % 512 >= 256, :, 17] = 1.0  # another group of the 4-bit format
+        if kind == "kv4":
+            pg = u.to_pages(*u.quantise_rows(rows.reshape(length, 64 * 128), 64))
+            kv.pool[torch.from_numpy(ids.astype(np.int64)).cuda(), 1, 0] = torch.from_numpy(pg).cuda()
+            k = u.from_pages(pg)
+            assert k[0, 0, 0] == 48 and k[300, 0, 17] > 0.9
+        else:
+            b = torch.from_numpy(rows).bfloat16().reshape(-1, 16, 64, 128)
+            kv.pool[torch.from_numpy(ids.astype(np.int64)).cuda(), 1, 0] = b.permute(0, 2, 1, 3).cuda()
+        unit = np.log2(np.e) / np.sqrt(128.0)              # base-2 score of a product
+        q = np.zeros((M, nq, 128), dtype=np.float32)
+        q[:, :, 0] = 2.0 ** exponent / unit / 48
+        q[:, :, 17] = rise / unit
+        sync()
+        got = attend(ctx, kv, kind, q, 0, 0).reshape(M, 64, nq // 64, 128)
+        top = np.abs(v[:length]).max(0)[None, :, None]
+        assert np.isfinite(got).all(), rise
+        # 512 products in up to three parts, 2 eps an addition
+        assert (np.abs(got) <= top * (1 + 3 * 512 * 2 * EPS)).all()
+    assert status(ctx) == 0
