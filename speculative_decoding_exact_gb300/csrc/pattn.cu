@@ -267,7 +267,7 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
       pair[h][r] = mx;
       named_bar(1 + ww, 64);
       mx = fmaxf(mx, pair[1 - h][r]);
-      const int e = min(max((int)((__float_as_uint(mx) >> 23) & 255u) - 127, -100), 100);
+      const int e = min(max((int)((__float_as_uint(mx) >> 23) & 255u) - 127, -100), 126);
       const float mul = 8.f * kScoreScale * __uint_as_float((uint32_t)(127 - e) << 23);
       unit = __uint_as_float((uint32_t)(124 + e) << 23);
 #pragma unroll

@@ -257,7 +257,7 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
     __syncthreads();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int e = min(max(((qmax[n + 8 * h] >> 23) & 255) - 127, -100), 100);
+      const int e = min(max(((qmax[n + 8 * h] >> 23) & 255) - 127, -100), 126);
       const float mul = __uint_as_float((uint32_t)(127 - e) << 23);
       unit[h] *= __uint_as_float((uint32_t)(127 + e) << 23);
       qv[h].x *= mul;

@@ -146,3 +146,10 @@ def test_large_scores_that_rise_a_little(kind, exponent, nq, M):
         # 512 products in up to three parts, 2 eps an addition
         assert (np.abs(got) <= top * (1 + 3 * 512 * 2 * EPS)).all()
     assert status(ctx) == 0
+
+
+@pytest.mark.parametrize("nq,M", [(2, 3), (26, 3), (26, 16)])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("q_exp", [116, 120, 124])
+def test_queries_of_any_size_that_fp32_holds(kind, q_exp, nq, M):
+    check_one_hot(kind, 2.0 ** q_exp, 2.0 ** -10, nq, M)
