@@ -47,13 +47,6 @@ constexpr int kThreads = 512;
 constexpr int kQWarps = 14;                         // all but the copying ones lay down Q
 constexpr int kQRows = (128 + kQWarps - 1) / kQWarps;
 
-// the upper 16 bits of two values, x0's in the low half; x becomes what is left
-SPEC_DEV uint32_t take_bf16(float& x0, float& x1) {
-  const uint32_t a = __float_as_uint(x0), b = __float_as_uint(x1);
-  x0 -= __uint_as_float(a & 0xFFFF0000u);
-  x1 -= __uint_as_float(b & 0xFFFF0000u);
-  return __byte_perm(a, b, 0x7632);
-}
 // one TMEM column (to be waited for)
 SPEC_DEV uint32_t tmem_ld1(uint32_t taddr) {
   uint32_t r;

@@ -33,9 +33,9 @@
 //
 // Precision: as pattn.cu for the 4-bit cache (binary16, q and p in two parts,
 // row-wise powers of two).  bf16 pages are operands as they are, with q and p in
-// three bf16 parts (24 significant bits): no value is out of range.  A unit's O is
-// added up in fp32, since the MMAs truncate: left in their accumulators over the 27
-// pages of a warp it was off by 1.2e-6 instead of 4e-7 (and 2.5 us faster).
+// three bf16 parts by truncation (24 significant bits): no value is out of range.
+// A unit's O is added up in fp32, since the MMAs truncate: left in their accumulators
+// over the 27 pages of a warp it was off by 1.2e-6 instead of 4e-7 (and 2.5 us faster).
 #include "attn_mma.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -89,11 +89,7 @@ SPEC_DEV uint32_t take_part(float& x0, float& x1) {
     minus_f16x2(x0, x1, *reinterpret_cast<const uint32_t*>(&h));
     return *reinterpret_cast<const uint32_t*>(&h);
   } else {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
-    const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
-    x0 -= __uint_as_float(u << 16);
-    x1 -= __uint_as_float(u & 0xFFFF0000u);
-    return u;
+    return take_bf16(x0, x1);
   }
 }
 

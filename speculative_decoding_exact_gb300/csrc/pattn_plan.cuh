@@ -87,6 +87,14 @@ SPEC_DEV void minus_f16x2(float& x0, float& x1, uint32_t h) {
       : "+f"(x0), "+f"(x1)
       : "r"(h));
 }
+// the upper 16 bits of two values, x0's in the low half; x becomes what is left
+// (by truncation: rounding would turn the largest numbers into infinities)
+SPEC_DEV uint32_t take_bf16(float& x0, float& x1) {
+  const uint32_t a = __float_as_uint(x0), b = __float_as_uint(x1);
+  x0 -= __uint_as_float(a & 0xFFFF0000u);
+  x1 -= __uint_as_float(b & 0xFFFF0000u);
+  return __byte_perm(a, b, 0x7632);
+}
 SPEC_DEV uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
 
 // Loads issued where they stand (a plain load may be moved down to its use, behind a

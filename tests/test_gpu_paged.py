@@ -153,3 +153,20 @@ def test_large_scores_that_rise_a_little(kind, exponent, nq, M):
 @pytest.mark.parametrize("q_exp", [116, 120, 124])
 def test_queries_of_any_size_that_fp32_holds(kind, q_exp, nq, M):
     check_one_hot(kind, 2.0 ** q_exp, 2.0 ** -10, nq, M)
+
+
+@pytest.mark.parametrize("nq,M", [(2, 3), (26, 3), (26, 16)])
+@pytest.mark.parametrize("kind", KINDS)
+def test_queries_next_to_the_largest_fp32_number(kind, nq, M):
+    """Elements that would round to infinity in bf16."""
+    ctx = context(nq, 2)
+    length = 700
+    kv, k, v, _ = cache(ctx, kind, length, 17, spread=2.0 ** -12)
+    rng = np.random.default_rng(3)
+    q = (rng.standard_normal((M, nq, 128)) * 2.0 ** 120).astype(np.float32)
+    q[:, :, ::16] = np.where(rng.random((M, nq, 8)) < 0.5, -1, 1) * np.finfo(np.float32).max
+    got = attend(ctx, kv, kind, q, 0, 0).reshape(M, nq, 128)
+    want, sure = one_hot(q, k, v, nq, length)
+    assert sure.mean() > 0.8
+    assert (np.abs(got - want)[sure] <= 4 * EPS * np.abs(want[sure])).all()
+    assert status(ctx) == 0
