@@ -424,7 +424,10 @@ SPEC_API int spec_attention(spec_ctx* ctx, const spec_kv* kv, int layer,
  * cheap view of a long context).  window = 0: every t <= p, sinks ignored.
  * 1 <= M <= 16; window, sinks >= 0.  A key on an unmapped page is not seen; a
  * row that sees no key (seq_len < M) is zero.  What a row does not see does not
- * reach it, NaN and infinities included.  With r = M * n_q_heads / n_kv_heads
+ * reach it, NaN and infinities included.  A V element that is not finite makes
+ * that output element of the rows that see it infinite (NaN for a NaN, where
+ * signs meet, or where its weight underflows) and changes no other; a row that
+ * sees a K element that is not finite is unspecified.  With r = M * n_q_heads / n_kv_heads
  * the query rows of a KV head, calls are of one kind for r <= 16 and of another
  * for every value of ceil(r / 128) above; row i's result is the same bits in
  * every call of a kind that places it at the same position, and differs by

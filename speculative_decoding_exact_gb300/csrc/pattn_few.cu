@@ -130,12 +130,10 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
   __shared__ uint4 qs[kParts][8][32];                   // A fragments
   __shared__ int qmax[kFewRows];
   __shared__ float2 ml_sm[kWarps][kFewRows];
-  __shared__ uint32_t poison;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = lane >> 2, g = lane & 3;
   const int slot = blockIdx.x, kvh = blockIdx.y, R = pl.M * pl.group;
   if (tid < kFewRows) qmax[tid] = 0;
-  if (tid == 32) poison = 0;
   uint8_t* ring = sm + warp * Ring::kWarp;
   pdl_wait();
   pdl_trigger();                                        // not before: see the merge in pattn.cu
@@ -273,8 +271,13 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
   }
   __syncthreads();
 
+  // An element of V that is not finite makes every row of its MMA infinite or NaN,
+  // the rows that do not see its key too.  Where that happened the pass is run again
+  // without such elements, and each is then added to the rows that see it: one rule
+  // for every row, whatever the others of its block see.
+  bool again = false;
 #pragma unroll 1
-  for (int pass = 0; pass < passes; ++pass) {
+  for (int pass = 0; pass < passes;) {
     const Span sp = span_of(pl, n_past, pass);
     bool mine[2];
 #pragma unroll
@@ -383,32 +386,24 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
                 const int t = k0 + 16 * pg + 4 * g + e;
                 if (!(((there >> pg) & 1u) && mine[h] && t <= pos[h] && (t >= plow[h] || t < sinks))) x[pg][h][e] = -INFINITY;
               }
-          if constexpr (!k4) {
-            // V rows that no row sees are zeroed (stale bytes may be anything,
-            // and 0 * NaN is NaN); a non-finite element that only some rows see
-            // is taken out, and those rows get it at the end
+        }
+        if constexpr (!k4) {
+          // V rows that no row sees are zeroed (stale bytes may be anything, and
+          // 0 * NaN is NaN), on a second pass every element that is not finite
+          if (masked || again) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int t = k0 + 4 * g + e;
               const bool seen = t <= b_last && (t >= low0 || t < sinks);
-              const bool by_all = t <= n_past && (t >= low1 || t < sinks);
-              bool bad = false;
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
                 uint32_t* w = reinterpret_cast<uint32_t*>(&v16[e][c]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                   const bool lo = (w[i] & 0x7F80u) == 0x7F80u, hi = (w[i] & 0x7F800000u) == 0x7F800000u;
-                  if (!seen) {
-                    w[i] = 0;
-                  } else if (!by_all && (lo || hi)) {
-                    bad = true;
-                    w[i] &= (lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0x0000FFFFu : 0xFFFFFFFFu);
-                  }
+                  w[i] = !seen ? 0u : !again ? w[i] : w[i] & (lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0x0000FFFFu : 0xFFFFFFFFu);
                 }
               }
-              // bit b: key n_past + 1 + b (b < 16) or low0 + b - 16
-              if (bad) atomicOr(&poison, 1u << (t > n_past ? t - n_past - 1 : 16 + t - low0));
             }
           }
         }
@@ -544,7 +539,7 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
         }
     }
     __syncthreads();
-    const uint32_t bad = k4 ? 0u : poison;
+    bool odd = false;                                   // a row is not finite
     const int r_lo = sp.i0 * pl.group, r_hi = min(sp.i1 * pl.group, R);
     for (int r = r_lo + (tid >> 5); r < r_hi; r += kWarps) {        // a warp per row, 4 d's per lane
       float m = -INFINITY;
@@ -567,26 +562,34 @@ pattn_few_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer
         y.z += a * z.z;
         y.w += a * z.w;
       }
-      const int p = n_past + r / pl.group, low = window_low(pl, p);
-      for (uint32_t left = bad; left; left &= left - 1) {
-        const int b = __ffs(left) - 1, t = b < 16 ? n_past + 1 + b : low0 + b - 16;
-        if (t > p || (t < low && t >= sinks)) continue;
-        const uint2 w = *reinterpret_cast<const uint2*>(vbase + (uint64_t)(uint32_t)page_at(kv, t >> 4) * stride + 256 * (t & 15) + 8 * lane);
-        const float v[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                            __uint_as_float(w.y & 0xFFFF0000u)};
-        if (!(fabsf(v[0]) <= 3.4e38f)) y.x += v[0];
-        if (!(fabsf(v[1]) <= 3.4e38f)) y.y += v[1];
-        if (!(fabsf(v[2]) <= 3.4e38f)) y.z += v[2];
-        if (!(fabsf(v[3]) <= 3.4e38f)) y.w += v[3];
+      if constexpr (!k4) {
+        odd = odd || !(fabsf(y.x) + fabsf(y.y) + fabsf(y.z) + fabsf(y.w) < INFINITY);
+        if (again) {
+          const int p = n_past + div24(r, pl.group), low = window_low(pl, p);
+          for (int j = 0; j < tl.n * kPagesPerTile; ++j) {
+            const int lp = tl.at(j / kPagesPerTile) * kPagesPerTile + j % kPagesPerTile, id = page_at(kv, lp);
+            if (!page_ok(kv, id)) continue;
+            const uint8_t* vp = vbase + (uint64_t)(uint32_t)id * stride + 8 * lane;
+            for (int t = 16 * lp; t < 16 * lp + 16; ++t, vp += 256) {
+              if (t > p || (t < low && t >= sinks)) continue;
+              const uint2 w = ldg_now(reinterpret_cast<const uint2*>(vp));
+              if ((w.x & 0x7F80u) == 0x7F80u) y.x += __uint_as_float(w.x << 16);
+              if ((w.x & 0x7F800000u) == 0x7F800000u) y.y += __uint_as_float(w.x & 0xFFFF0000u);
+              if ((w.y & 0x7F80u) == 0x7F80u) y.z += __uint_as_float(w.y << 16);
+              if ((w.y & 0x7F800000u) == 0x7F800000u) y.w += __uint_as_float(w.y & 0xFFFF0000u);
+            }
+          }
+        }
       }
       const size_t at = ((size_t)slot * pl.nkv + kvh) * R + r;
       reinterpret_cast<float4*>(part_o)[(((size_t)slot * pl.nkv + kvh) * 32 + lane) * R + r] = y;
       if (lane == 0) part_ml[at] = make_float2(m, L);
     }
-    if (pass + 1 < passes) {
-      __syncthreads();                                  // the shared memory is free for the next pass
-      start(1);
-    }
+    // the barrier also frees the shared memory for the next pass
+    const bool found = __syncthreads_or(odd);
+    again = found && !again;
+    if (!again) ++pass;
+    if (pass < passes) start(pass);
   }
 }
 

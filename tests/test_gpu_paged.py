@@ -170,3 +170,45 @@ def test_queries_next_to_the_largest_fp32_number(kind, nq, M):
     assert sure.mean() > 0.8
     assert (np.abs(got - want)[sure] <= 4 * EPS * np.abs(want[sure])).all()
     assert status(ctx) == 0
+
+# ---------------------------------------------------------------------------
+# infinite values
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("window,sinks", [(0, 0), (150, 20)])
+@pytest.mark.parametrize("nq,M", [(2, 16), (4, 4), (26, 16), (26, 9)])
+def test_infinite_v_elements_reach_the_rows_that_see_them_alike(nq, M, window, sinks):
+    """An infinite V element makes that output element of every row that sees it
+    infinite, of its sign, NaN where signs meet; the row's other elements keep their
+    bits; and the rows have the same bits in a smaller block."""
+    ctx = context(nq, 2)
+    length = 700
+    kv, _, _, ids = cache(ctx, "bf16", length, 81)
+    q = np.random.default_rng(8).standard_normal((M, nq, 128)).astype(np.float32)
+    clean = attend(ctx, kv, "bf16", q, window, sinks).reshape(M, nq, 128)
+    see = u.visible(M, length, window, sinks)
+    inf, nan = float("inf"), float("nan")
+    low = length - M - window + 1 if window else 300                       # the first row's first key
+    spots = [[(length - M - 3, 5, inf)],                                   # seen by every row
+             [(length - M - 3, 5, -inf), (low + 40, 127, inf)],
+             [(length - 2, 64, -inf)],                                     # by the last two
+             [(low + 1, 0, inf), (3, 17, -inf)],                           # by the first two (of a window); a sink
+             [(length - M - 3, 9, inf), (length - 5, 9, -inf)],            # signs that meet in some rows
+             [(length - M - 9, 77, nan), (length - 1, 78, inf)]]
+    for spot in spots:
+        saved = kv.pool.clone()
+        want = np.zeros((M, 128))
+        for t, d, val in spot:
+            kv.pool[int(ids[t // 16]), 1, 1, :, t % 16, d] = val
+            with np.errstate(invalid="ignore"):
+                want[:, d] += np.where(see[:, t], val, 0.0)
+        got = attend(ctx, kv, "bf16", q, window, sinks).reshape(M, nq, 128)
+        odd = np.broadcast_to((want != 0)[:, None], got.shape)             # NaN too
+        assert same_bits(np.where(odd, np.float32(0), got), np.where(odd, np.float32(0), clean)), spot
+        assert np.array_equal(got[odd], np.broadcast_to(want[:, None], got.shape)[odd], equal_nan=True), spot
+        for i, m in ((M - 1, 1), (M // 2, 2)) if nq < 26 else ((M - 2, 2), (M - 8, 8)) if M <= 9 else ((6, 10),):
+            kv.seq_len[0] = length - M + i + m
+            part = attend(ctx, kv, "bf16", q[i:i + m], window, sinks).reshape(m, nq, 128)
+            assert np.array_equal(part, got[i:i + m], equal_nan=True), (spot, i, m)
+        kv.seq_len[0] = length
+        kv.pool.copy_(saved)
+    assert status(ctx) == 0
