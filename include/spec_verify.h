@@ -207,6 +207,11 @@ typedef struct spec_weights {
  * is refused (SPEC_ST_ROLLBACK): the ring may no longer hold the rows a
  * window would need.  The paged pool's slices of sliding-window layers are
  * not used. */
+#define SPEC_KV_ANY  0   /* not said: taken by every call                       */
+#define SPEC_KV_BF16 1   /* the pool above; calls on 4-bit pages refuse it      */
+#define SPEC_KV_4BIT 2   /* 4-bit pages (see SPEC_KV4_PAGE_BYTES); the steps,
+                            spec_attention and spec_attention_window refuse it
+                            (SPEC_EINVAL): they would reach past the pool      */
 #define SPEC_SWA_RING_ROWS(W) ((((W) + 15) / 16) * 16 + 16)
 
 typedef struct spec_kv {
@@ -219,6 +224,7 @@ typedef struct spec_kv {
     int32_t* free_top;
     void*    swa_ring;
     int32_t* swa_state;
+    int32_t  kind;         /* SPEC_KV_*: what the pool holds */
 } spec_kv;
 
 /* Step result, DEVICE memory written by the accept kernel at the end of the
@@ -456,7 +462,8 @@ SPEC_API int spec_attention_window(spec_ctx* ctx, const spec_kv* kv, int layer, 
 SPEC_API int spec_qk_norm_rope(spec_ctx* ctx, const float* x, int ldx, int n, const int32_t* pos,
                                const float* q_norm, const float* k_norm, float* out, int ldo);
 
-/* ---- 4-bit KV cache.  A spec_kv whose pool holds 4-bit pages:
+/* ---- 4-bit KV cache.  A spec_kv whose pool holds 4-bit pages (its kind, where
+ * said, is SPEC_KV_4BIT):
  *   pool  uint8 [num_pages][n_layers][2 (K,V)][n_kv_heads][SPEC_KV4_PAGE_BYTES]
  * with the page table, length and free stack of any other cache, so
  * spec_kv_reset, spec_kv_extend and spec_kv_rollback serve it as they are.

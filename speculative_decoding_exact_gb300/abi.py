@@ -18,6 +18,7 @@ SPEC_OK, SPEC_EINVAL, SPEC_EVERIFYLEN, SPEC_ENULL, SPEC_EALIGN = 0, -1, -2, -3, 
 SPEC_ENOMEM, SPEC_ECAPACITY, SPEC_ECUDA, SPEC_ENODEV = -5, -6, -7, -8
 ST_TOKEN_RANGE, ST_NONFINITE, ST_POOL_EMPTY, ST_ROLLBACK, ST_CTX_FULL = 1, 2, 4, 8, 16
 ST_DEVICE_WAIT, ST_BAD_TREE = 0x20, 0x40
+KV_ANY, KV_BF16, KV_4BIT = 0, 1, 2
 
 
 class spec_config(C.Structure):
@@ -38,7 +39,7 @@ class spec_weights(C.Structure):
 class spec_kv(C.Structure):
     _fields_ = [("pool", C.c_void_p), ("num_pages", C.c_int32), ("max_seq_pages", C.c_int32),
                 ("page_table", C.c_void_p), ("seq_len", C.c_void_p), ("free_stack", C.c_void_p),
-                ("free_top", C.c_void_p), ("swa_ring", C.c_void_p), ("swa_state", C.c_void_p)]
+                ("free_top", C.c_void_p), ("swa_ring", C.c_void_p), ("swa_state", C.c_void_p), ("kind", C.c_int32)]
 
 
 class spec_result(C.Structure):

@@ -133,6 +133,11 @@ int check_kv(const spec_kv* kv) {
   return SPEC_OK;
 }
 
+// the cache says that its pool holds the other kind of pages; checked last, so that
+// a call with several faults has the code of the others
+bool holds_4bit(const spec_kv* kv) { return kv->kind == SPEC_KV_4BIT; }
+bool holds_bf16(const spec_kv* kv) { return kv->kind == SPEC_KV_BF16; }
+
 int check_kv_swa(const spec_ctx* c, const spec_kv* kv) {
   if (!has_swa(c->cfg)) return SPEC_OK;
   if (!kv->swa_ring || !kv->swa_state) return SPEC_ENULL;
@@ -475,6 +480,7 @@ int spec_attention(spec_ctx* c, const spec_kv* kv, int layer, const float* q, in
     return SPEC_ECAPACITY;   // attention workspace must cover every position the cache can hold
   }
   if (!aligned(q) || !aligned(out)) return SPEC_EALIGN;
+  if (holds_4bit(kv)) return SPEC_EINVAL;
   const AttnPlan& ap = ring ? c->attn_swa : c->attn;
   SPEC_TRY(cudaMemsetAsync(c->status, 0, 4, c->stream));
   SPEC_TRY(launch_q_to_tile(q, M, ap, c->qtile, c->stream, false));
@@ -510,6 +516,7 @@ static int paged_attention(spec_ctx* c, bool k4, const spec_kv* kv, int layer, c
   if (!aligned(q) || !aligned(out)) return SPEC_EALIGN;
   const size_t bytes = span_bytes(M, c->cfg.n_q_heads * 128, c->cfg.n_q_heads * 128);
   if (overlap(q, bytes, out, bytes)) return SPEC_EINVAL;
+  if (k4 ? holds_bf16(kv) : holds_4bit(kv)) return SPEC_EINVAL;
   return cuda_code(launch_paged_attention(k4, v, layer, q, M, c->cfg.n_q_heads, window, sinks, c->num_sms, c->attn_part,
                                           out, c->status, c->stream));
 }
@@ -551,6 +558,7 @@ static int check_kv4_rows(spec_ctx* c, const spec_kv* kv, int layer, const float
   if (layer < 0 || layer >= c->cfg.n_layers || n < 0) return SPEC_EINVAL;
   if (ld < c->cfg.n_kv_heads * c->cfg.head_dim || ld % 4) return SPEC_EINVAL;
   if (!aligned(k) || !aligned(v)) return SPEC_EALIGN;
+  if (holds_bf16(kv)) return SPEC_EINVAL;
   return SPEC_OK;
 }
 
@@ -853,6 +861,7 @@ static int run_step(spec_ctx* c, const spec_weights* w, spec_kv* kv, const float
   if (!aligned(hidden)) return SPEC_EALIGN;
   if (kv->max_seq_pages * c->cfg.page_size > c->attn.max_chunks * c->attn.chunk)
     return SPEC_ECAPACITY;   // attention workspace must cover every position the cache can hold
+  if (holds_4bit(kv)) return SPEC_EINVAL;
 
   // Steps with taps, with GEMM profiling, or on the legacy default stream
   // (which cannot be captured) are enqueued directly.
@@ -988,6 +997,7 @@ int spec_verify_step_host(spec_ctx* c, const spec_weights* w, spec_kv* kv, const
   if (!c || !hidden_host || !draft_host || !res_host) return SPEC_ENULL;
   if (k != 3 && k != 7 && k != 15) return SPEC_EVERIFYLEN;
   if (k + 1 > c->cfg.max_rows) return SPEC_ECAPACITY;
+  if (kv && holds_4bit(kv)) return SPEC_EINVAL;
   const size_t hb = sizeof(float) * (size_t)(k + 1) * c->cfg.hidden;
   SPEC_TRY(cudaMemcpyAsync(c->hidden_dev, hidden_host, hb, cudaMemcpyHostToDevice, c->stream));
   SPEC_TRY(cudaMemcpyAsync(c->draft_dev, draft_host, sizeof(int32_t) * k, cudaMemcpyHostToDevice,

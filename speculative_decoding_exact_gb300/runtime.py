@@ -123,26 +123,25 @@ class DeviceWeights:
                                 ptr(self.final_norm), ptr(self.w_head), arr(self.q_norm), arr(self.k_norm))
 
 
-class DeviceKV:
-    """Paged bf16 KV cache and its metadata, all in device memory."""
-
-    def __init__(self, cfg: ModelConfig, num_pages: int, max_seq_pages: int):
-        self.cfg = cfg
-        self.pool = torch.zeros((num_pages, cfg.n_layers, 2, cfg.n_kv_heads, cfg.page_size,
-                                 cfg.head_dim), dtype=torch.bfloat16, device="cuda")
-        self._init_metadata(num_pages, max_seq_pages)
+class PagedKV:
+    """The metadata of a paged cache in device memory, whatever its pages hold.  A
+    subclass allocates `pool` and says with KIND what that is."""
+    KIND = abi.KV_ANY
 
     def _init_metadata(self, num_pages: int, max_seq_pages: int):
-        cfg = self.cfg
         self.page_table = torch.full((max_seq_pages,), -1, dtype=torch.int32, device="cuda")
         self.seq_len = torch.zeros(4, dtype=torch.int32, device="cuda")
         self.free_stack = torch.zeros(num_pages, dtype=torch.int32, device="cuda")
         self.free_top = torch.zeros(4, dtype=torch.int32, device="cuda")
         self.num_pages = num_pages
         self.max_seq_pages = max_seq_pages
+        self.swa_ring = self.swa_state = None
+        self._init_rings()
+
+    def _init_rings(self):
         # sliding-window layers: ring [n_swa][K,V][n_kv][R][dh] (R = W rounded up
         # to 16, plus 16 spare slots) and the last block's state
-        self.swa_ring = self.swa_state = None
+        cfg = self.cfg
         if cfg.n_swa > 0:
             self.swa_ring = torch.zeros((cfg.n_swa, 2, cfg.n_kv_heads, cfg.swa_ring_rows, cfg.head_dim),
                                         dtype=torch.bfloat16, device="cuda")
@@ -152,7 +151,35 @@ class DeviceKV:
         return abi.spec_kv(self.pool.data_ptr(), self.num_pages, self.max_seq_pages,
                            self.page_table.data_ptr(), self.seq_len.data_ptr(),
                            self.free_stack.data_ptr(), self.free_top.data_ptr(),
-                           ptr(self.swa_ring), ptr(self.swa_state))
+                           ptr(self.swa_ring), ptr(self.swa_state), self.KIND)
+
+    def reset(self, ctx: Context):
+        abi.check("spec_kv_reset", abi.spec_kv_reset(ctx.h, self.struct()))
+
+    def extend(self, ctx: Context, n: int):
+        abi.check("spec_kv_extend", abi.spec_kv_extend(ctx.h, self.struct(), n))
+
+    def rollback(self, ctx: Context, new_len: int):
+        abi.check("spec_kv_rollback", abi.spec_kv_rollback(ctx.h, self.struct(), new_len))
+
+    def state(self):
+        """(seq_len, mapped page ids, unmapped tail, free stack) read back to the host."""
+        n = int(self.seq_len[0].item())
+        pt = self.page_table.cpu().numpy()
+        top = int(self.free_top[0].item())
+        pages = (n + self.cfg.page_size - 1) // self.cfg.page_size
+        return n, pt[:pages].copy(), pt[pages:].copy(), self.free_stack[:top].cpu().numpy()
+
+
+class DeviceKV(PagedKV):
+    """Paged bf16 KV cache and its metadata, all in device memory."""
+    KIND = abi.KV_BF16
+
+    def __init__(self, cfg: ModelConfig, num_pages: int, max_seq_pages: int):
+        self.cfg = cfg
+        self.pool = torch.zeros((num_pages, cfg.n_layers, 2, cfg.n_kv_heads, cfg.page_size,
+                                 cfg.head_dim), dtype=torch.bfloat16, device="cuda")
+        self._init_metadata(num_pages, max_seq_pages)
 
     def write_ring_rows(self, layer: int, pos0: int, k_bits: np.ndarray, v_bits: np.ndarray):
         """Write bf16 bit patterns [n][n_kv*dh] of positions pos0.. of a
@@ -172,23 +199,6 @@ class DeviceKV:
         s = self.cfg.swa_index(layer)
         slots = np.asarray(positions) % self.cfg.swa_ring_rows
         return self.swa_ring.view(torch.int16)[s][:, :, slots, :].cpu().numpy().view(np.uint16)
-
-    def reset(self, ctx: Context):
-        abi.check("spec_kv_reset", abi.spec_kv_reset(ctx.h, self.struct()))
-
-    def extend(self, ctx: Context, n: int):
-        abi.check("spec_kv_extend", abi.spec_kv_extend(ctx.h, self.struct(), n))
-
-    def rollback(self, ctx: Context, new_len: int):
-        abi.check("spec_kv_rollback", abi.spec_kv_rollback(ctx.h, self.struct(), new_len))
-
-    def state(self):
-        """(seq_len, mapped page ids, unmapped tail, free stack) read back to the host."""
-        n = int(self.seq_len[0].item())
-        pt = self.page_table.cpu().numpy()
-        top = int(self.free_top[0].item())
-        pages = (n + self.cfg.page_size - 1) // self.cfg.page_size
-        return n, pt[:pages].copy(), pt[pages:].copy(), self.free_stack[:top].cpu().numpy()
 
     def write_rows(self, layer: int, pos0: int, k_bits: np.ndarray, v_bits: np.ndarray):
         """Write bf16 bit patterns [n][n_kv*dh] for positions pos0.. of one layer."""
@@ -218,9 +228,10 @@ class DeviceKV:
             pool16[page, layer, 1, :, : b - a, :] = vb[a:b].permute(1, 0, 2)
 
 
-class DeviceKV4(DeviceKV):
+class DeviceKV4(PagedKV):
     """Paged 4-bit KV cache: the same metadata, pages of abi.KV4_PAGE_BYTES bytes
     (spec_kv4_append writes them, spec_attention_kv4 reads them)."""
+    KIND = abi.KV_4BIT
 
     def __init__(self, cfg: ModelConfig, num_pages: int, max_seq_pages: int):
         self.cfg = cfg

@@ -1,0 +1,87 @@
+"""What the entry points and runtime classes refuse and allow around the two paged
+caches."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+from speculative_decoding_exact_gb300 import abi, runtime, synth  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def config(nq=4, nkv=2, **kw):
+    return runtime.ModelConfig(hidden=512, n_layers=2, n_q_heads=nq, n_kv_heads=nkv, head_dim=128, ffn=512, vocab=512,
+                               **kw)
+
+
+def sync():
+    torch.cuda.synchronize()
+
+
+def weights(ctx):
+    cfg = ctx.cfg
+    w = runtime.DeviceWeights(cfg)
+    for i in range(cfg.n_layers):
+        for j, (name, N, K) in enumerate(cfg.matrices()):
+            getattr(w, name).append(runtime.upload_tiled(ctx, synth.q4k_matrix(N, K, i, j), N, K))
+    w.w_head = runtime.upload_tiled(ctx, synth.q4k_matrix(cfg.vocab, cfg.hidden, 9, 9), cfg.vocab, cfg.hidden)
+    return w
+
+
+def test_a_cache_of_the_other_kind_is_refused():
+    """A 4-bit pool has smaller pages than a bf16 one: a call that took it for bf16 rows
+    would reach past it.  (Large enough here that nothing would.)"""
+    cfg = config()
+    ctx = runtime.Context(cfg, max_ctx=128)
+    w = weights(ctx)
+    big = torch.zeros(8 * 2 * 2 * 2 * 4096, dtype=torch.uint8, device="cuda")
+    kv = {abi.KV_BF16: runtime.DeviceKV(cfg, 8, 8), abi.KV_4BIT: runtime.DeviceKV4(cfg, 8, 8)}
+    kv[abi.KV_4BIT].pool = big
+    hidden, q, out, k, v = (torch.zeros(16, 512, device="cuda") for _ in range(5))
+    draft = torch.zeros(15, dtype=torch.int32, device="cuda")
+    parent = torch.tensor([-1, 0, 0], dtype=torch.int32, device="cuda")
+    probs = torch.full((3, cfg.vocab), 1.0 / cfg.vocab, device="cuda")
+    mt = torch.zeros(abi.MT_WORDS + 3, dtype=torch.int32, device="cuda")
+    res = torch.zeros(4, dtype=torch.int32, device="cuda")
+    hh, dh, rh = torch.zeros(4, 512), torch.zeros(3, dtype=torch.int32), abi.spec_result()
+    h, p = ctx.h, lambda t: t.data_ptr()
+    calls = {
+        "step": (abi.KV_BF16, lambda s: abi.spec_verify_step(h, w.struct(), s, p(hidden), p(draft), 3, p(res))),
+        "step_ex": (abi.KV_BF16, lambda s: abi.spec_verify_step_ex(h, w.struct(), s, p(hidden), p(draft), 3, p(res), None)),
+        "step_host": (abi.KV_BF16, lambda s: abi.spec_verify_step_host(h, w.struct(), s, p(hh), p(dh), 3, rh)),
+        "sampled": (abi.KV_BF16, lambda s: abi.spec_verify_step_sampled(h, w.struct(), s, p(hidden), p(draft), p(probs), 3,
+                                                                        p(mt), p(res), None)),
+        "tree": (abi.KV_BF16, lambda s: abi.spec_verify_tree(h, w.struct(), s, p(hidden), p(draft), p(parent), 3, p(res),
+                                                             None, None)),
+        "attention": (abi.KV_BF16, lambda s: abi.spec_attention(h, s, 1, p(q), 2, p(out))),
+        "window": (abi.KV_BF16, lambda s: abi.spec_attention_window(h, s, 1, p(q), 2, 0, 0, p(out))),
+        "kv4": (abi.KV_4BIT, lambda s: abi.spec_attention_kv4(h, s, 1, p(q), 2, 0, 0, p(out))),
+        "append": (abi.KV_4BIT, lambda s: abi.spec_kv4_append(h, s, 1, p(k), p(v), 512, 2)),
+        "read": (abi.KV_4BIT, lambda s: abi.spec_kv4_read(h, s, 1, 0, 2, p(k), p(v), 512)),
+    }
+    for c in kv.values():
+        c.reset(ctx)
+        c.extend(ctx, 5)                                   # the metadata calls take either
+        c.rollback(ctx, 4)
+    for name, (takes, call) in calls.items():
+        for kind, c in kv.items():
+            before, lengths = c.pool.clone(), c.seq_len.clone()
+            s = c.struct()
+            assert s.kind == kind
+            if kind == takes:
+                assert call(s) == abi.SPEC_OK, name
+                sync()
+                c.rollback(ctx, 4)
+                sync()
+                abi.spec_last_status(ctx.h)
+            else:
+                assert call(s) == abi.SPEC_EINVAL, name
+                sync()
+                assert torch.equal(before, c.pool) and torch.equal(lengths, c.seq_len)
+    ctx.close()
