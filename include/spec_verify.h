@@ -206,7 +206,8 @@ typedef struct spec_weights {
  * checkpoint).  A rollback below the last step's block, or after an extend,
  * is refused (SPEC_ST_ROLLBACK): the ring may no longer hold the rows a
  * window would need.  The paged pool's slices of sliding-window layers are
- * not used. */
+ * not used.  spec_kv_reset, spec_kv_extend and spec_kv_rollback also take a
+ * cache with both pointers NULL; the steps refuse it (SPEC_ENULL). */
 #define SPEC_KV_ANY  0   /* not said: taken by every call                       */
 #define SPEC_KV_BF16 1   /* the pool above; calls on 4-bit pages refuse it      */
 #define SPEC_KV_4BIT 2   /* 4-bit pages (see SPEC_KV4_PAGE_BYTES); the steps,
@@ -468,7 +469,8 @@ SPEC_API int spec_qk_norm_rope(spec_ctx* ctx, const float* x, int ldx, int n, co
  * with the page table, length and free stack of any other cache, so
  * spec_kv_reset, spec_kv_extend and spec_kv_rollback serve it as they are.
  * Every layer has its pages (the rings of sliding-window layers hold bf16
- * rows and are not used here).  A page holds 16 positions of one head:
+ * rows and are not used here: swa_ring and swa_state may be NULL on any ctx,
+ * and a rollback then goes to any length).  A page holds 16 positions of one head:
  *   byte 256*c + 16*t + j  codes of elements 32c+2j (low nibble) and 32c+2j+1
  *                          of position t (c < 4, j < 16)
  *   byte 1024 + 8*t + g    scale of elements 16g..16g+15 of position t

@@ -145,6 +145,12 @@ int check_kv_swa(const spec_ctx* c, const spec_kv* kv) {
   return SPEC_OK;
 }
 
+// for the calls that touch the metadata alone: a cache may come without the rings
+// (4-bit pages serve every layer), but not with half of them
+int check_kv_meta(const spec_ctx* c, const spec_kv* kv) {
+  return kv->swa_ring || kv->swa_state ? check_kv_swa(c, kv) : SPEC_OK;
+}
+
 int check_cfg(const spec_config* c) {
   if (!c) return SPEC_ENULL;
   if (c->hidden <= 0 || c->hidden % 256 || c->hidden / 256 > 64) return SPEC_EINVAL;
@@ -600,7 +606,7 @@ int spec_kv_reset(spec_ctx* c, spec_kv* kv) {
   if (!c) return SPEC_ENULL;
   int rc = check_kv(kv);
   if (rc) return rc;
-  rc = check_kv_swa(c, kv);
+  rc = check_kv_meta(c, kv);
   if (rc) return rc;
   return cuda_code(launch_kv_reset(view_of(c, kv), c->stream));
 }
@@ -609,7 +615,7 @@ int spec_kv_extend(spec_ctx* c, spec_kv* kv, int32_t n) {
   if (!c) return SPEC_ENULL;
   int rc = check_kv(kv);
   if (rc) return rc;
-  rc = check_kv_swa(c, kv);
+  rc = check_kv_meta(c, kv);
   if (rc) return rc;
   if (n < 0) return SPEC_EINVAL;
   return cuda_code(launch_kv_reserve(view_of(c, kv), n, 1, nullptr, 0, 0, c->status, nullptr,
@@ -621,7 +627,7 @@ int spec_kv_rollback(spec_ctx* c, spec_kv* kv, int32_t new_len) {
   int rc = check_kv(kv);
   if (rc) return rc;
   if (new_len < 0) return SPEC_EINVAL;
-  rc = check_kv_swa(c, kv);
+  rc = check_kv_meta(c, kv);
   if (rc) return rc;
   return cuda_code(launch_kv_rollback(view_of(c, kv), new_len, c->status, c->stream));
 }

@@ -669,8 +669,9 @@ __global__ void kv_rollback_kernel(KvView kv, int new_len, int32_t* status) {
   const int len = *kv.seq_len;
   bool bad = new_len < 0 || new_len > len;
   // a sliding-window ring can be wound back only over the rows its spare
-  // slots keep: to lengths at or above the last step's n_past
-  if (swa_layers(kv) > 0 && new_len < len && (kv.swa_state[0] < 0 || new_len < kv.swa_state[0])) bad = true;
+  // slots keep: to lengths at or above the last step's n_past (a cache without
+  // rings: to any)
+  if (swa_layers(kv) > 0 && kv.swa_state && new_len < len && (kv.swa_state[0] < 0 || new_len < kv.swa_state[0])) bad = true;
   if (bad) {
     atomicOr(status, SPEC_ST_ROLLBACK);
     return;

@@ -136,16 +136,6 @@ class PagedKV:
         self.num_pages = num_pages
         self.max_seq_pages = max_seq_pages
         self.swa_ring = self.swa_state = None
-        self._init_rings()
-
-    def _init_rings(self):
-        # sliding-window layers: ring [n_swa][K,V][n_kv][R][dh] (R = W rounded up
-        # to 16, plus 16 spare slots) and the last block's state
-        cfg = self.cfg
-        if cfg.n_swa > 0:
-            self.swa_ring = torch.zeros((cfg.n_swa, 2, cfg.n_kv_heads, cfg.swa_ring_rows, cfg.head_dim),
-                                        dtype=torch.bfloat16, device="cuda")
-            self.swa_state = torch.full((4,), -1, dtype=torch.int32, device="cuda")
 
     def struct(self) -> abi.spec_kv:
         return abi.spec_kv(self.pool.data_ptr(), self.num_pages, self.max_seq_pages,
@@ -180,6 +170,16 @@ class DeviceKV(PagedKV):
         self.pool = torch.zeros((num_pages, cfg.n_layers, 2, cfg.n_kv_heads, cfg.page_size,
                                  cfg.head_dim), dtype=torch.bfloat16, device="cuda")
         self._init_metadata(num_pages, max_seq_pages)
+
+    def _init_metadata(self, num_pages: int, max_seq_pages: int):
+        super()._init_metadata(num_pages, max_seq_pages)
+        # sliding-window layers: ring [n_swa][K,V][n_kv][R][dh] (R = W rounded up
+        # to 16, plus 16 spare slots) and the last block's state
+        cfg = self.cfg
+        if cfg.n_swa > 0:
+            self.swa_ring = torch.zeros((cfg.n_swa, 2, cfg.n_kv_heads, cfg.swa_ring_rows, cfg.head_dim),
+                                        dtype=torch.bfloat16, device="cuda")
+            self.swa_state = torch.full((4,), -1, dtype=torch.int32, device="cuda")
 
     def write_ring_rows(self, layer: int, pos0: int, k_bits: np.ndarray, v_bits: np.ndarray):
         """Write bf16 bit patterns [n][n_kv*dh] of positions pos0.. of a

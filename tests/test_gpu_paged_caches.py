@@ -1,5 +1,6 @@
 """What the entry points and runtime classes refuse and allow around the two paged
 caches."""
+import numpy as np
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -7,6 +8,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 from speculative_decoding_exact_gb300 import abi, runtime, synth  # noqa: E402
+from tests import kv4_util as u  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -84,4 +86,56 @@ def test_a_cache_of_the_other_kind_is_refused():
                 assert call(s) == abi.SPEC_EINVAL, name
                 sync()
                 assert torch.equal(before, c.pool) and torch.equal(lengths, c.seq_len)
+    ctx.close()
+
+
+def test_a_4bit_cache_beside_sliding_window_layers():
+    """On a context with sliding-window layers a 4-bit cache needs no rings: reset,
+    extend, append, attention on a ring layer and rollback, which reaches any length."""
+    nq, nkv = 4, 2
+    ctx = runtime.Context(config(nq, nkv, swa_window=32, swa_period=2), max_ctx=256)
+    kv = runtime.DeviceKV4(ctx.cfg, 16, 16)
+    assert kv.swa_ring is None and kv.swa_state is None
+    kv.reset(ctx)
+    kv.extend(ctx, 100)
+    rows = np.random.default_rng(1).standard_normal((100, 2 * nkv * 128)).astype(np.float32)
+    x = torch.from_numpy(rows).cuda()
+    kv.append(ctx, 1, x[:, :nkv * 128], x[:, nkv * 128:])
+    held = [u.code_values()[c] * u.scale_values()[b].repeat(16, -1)
+            for c, b in (u.quantise_rows(rows[:, i * nkv * 128:(i + 1) * nkv * 128], nkv) for i in range(2))]
+    q = np.random.default_rng(2).standard_normal((3, nq, 128)).astype(np.float32)
+    qd = torch.from_numpy(q).cuda()
+    out = torch.empty((3, nq * 128), device="cuda")
+    for length in (100, 90, 20, 100):                      # back, further back, and forward again
+        if length < 100 or int(kv.seq_len[0]) == 100:
+            kv.rollback(ctx, length)
+        else:
+            kv.extend(ctx, length - int(kv.seq_len[0]))
+        abi.check("attention", abi.spec_attention_kv4(ctx.h, kv.struct(), 1, qd.data_ptr(), 3, 40, 4, out.data_ptr()))
+        sync()
+        assert int(kv.seq_len[0]) == length
+        want, bound = u.attention(q, held[0], held[1], nq, 40, 4, length)
+        assert (np.abs(out.cpu().numpy() - want) <= bound).all()
+    assert abi.spec_last_status(ctx.h) == 0
+    # bf16: the metadata calls go without rings too, half of them or a step do not
+    bf = runtime.DeviceKV(ctx.cfg, 16, 16)
+    s = bf.struct()
+    w = weights(ctx)
+    hidden, draft = torch.zeros(4, 512, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    res = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for ring, state in ((None, s.swa_state), (s.swa_ring, None)):
+        half = bf.struct()
+        half.swa_ring, half.swa_state = ring, state
+        assert abi.spec_kv_reset(ctx.h, half) == abi.spec_kv_extend(ctx.h, half, 1) == abi.SPEC_ENULL
+        assert abi.spec_kv_rollback(ctx.h, half, 0) == abi.SPEC_ENULL
+    s.swa_ring = s.swa_state = None
+    assert abi.spec_kv_reset(ctx.h, s) == abi.spec_kv_extend(ctx.h, s, 8) == abi.SPEC_OK
+    assert abi.spec_verify_step(ctx.h, w.struct(), s, hidden.data_ptr(), draft.data_ptr(), 3, res.data_ptr()) == abi.SPEC_ENULL
+    assert abi.spec_attention(ctx.h, s, 1, hidden.data_ptr(), 2, hidden.data_ptr()) == abi.SPEC_ENULL
+    sync()
+    # a cache with rings keeps its limit: no rollback below an extend
+    bf.reset(ctx)
+    bf.extend(ctx, 60)
+    bf.rollback(ctx, 59)
+    assert abi.spec_last_status(ctx.h) == abi.ST_ROLLBACK and int(bf.seq_len[0]) == 60
     ctx.close()
