@@ -239,16 +239,33 @@ class DeviceKV4(PagedKV):
                                 dtype=torch.uint8, device="cuda")
         self._init_metadata(num_pages, max_seq_pages)
 
+    def _check_rows(self, name: str, x: torch.Tensor):
+        w = self.cfg.n_kv_heads * self.cfg.head_dim
+        if x.dtype != torch.float32 or x.dim() != 2 or x.shape[1] != w or not x.is_cuda:
+            raise ValueError(f"{name}: fp32 rows [n][{w}] on the GPU expected, not {x.dtype} {tuple(x.shape)} on {x.device}")
+        if x.shape[0] > 0 and x.stride(1) != 1:
+            raise ValueError(f"{name}: a row's values must lie side by side")
+
     def append(self, ctx: Context, layer: int, k: torch.Tensor, v: torch.Tensor):
         """Quantise fp32 rows [n][n_kv*dh] (row stride shared by k and v) into
         the last n positions, which extend() has mapped."""
-        assert k.stride(0) == v.stride(0) and k.shape == v.shape and k.stride(1) == v.stride(1) == 1
-        abi.check("spec_kv4_append", abi.spec_kv4_append(ctx.h, self.struct(), layer, ptr(k), ptr(v), k.stride(0),
-                                                         k.shape[0]))
+        self._check_rows("k", k)
+        self._check_rows("v", v)
+        n, w = k.shape
+        if v.shape[0] != n or (n > 1 and k.stride(0) != v.stride(0)):
+            raise ValueError(f"k and v: as many rows with one stride expected, not {n} by {k.stride(0)} and "
+                             f"{v.shape[0]} by {v.stride(0)}")
+        if n == 0:
+            return                                          # an empty tensor has no address
+        abi.check("spec_kv4_append", abi.spec_kv4_append(ctx.h, self.struct(), layer, ptr(k), ptr(v),
+                                                         k.stride(0) if n > 1 else w, n))
 
     def read(self, ctx: Context, layer: int, pos0: int, n: int):
         """fp32 (k, v) rows [n][n_kv*dh] of positions pos0 .. pos0+n-1."""
+        if n < 0:
+            raise ValueError(f"n: at least 0 rows, not {n}")
         w = self.cfg.n_kv_heads * self.cfg.head_dim
         k, v = torch.empty((n, w), device="cuda"), torch.empty((n, w), device="cuda")
-        abi.check("spec_kv4_read", abi.spec_kv4_read(ctx.h, self.struct(), layer, pos0, n, ptr(k), ptr(v), w))
+        if n > 0:
+            abi.check("spec_kv4_read", abi.spec_kv4_read(ctx.h, self.struct(), layer, pos0, n, ptr(k), ptr(v), w))
         return k, v

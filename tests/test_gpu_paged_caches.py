@@ -139,3 +139,26 @@ def test_a_4bit_cache_beside_sliding_window_layers():
     bf.rollback(ctx, 59)
     assert abi.spec_last_status(ctx.h) == abi.ST_ROLLBACK and int(bf.seq_len[0]) == 60
     ctx.close()
+
+
+def test_append_of_single_rows_and_other_strides():
+    ctx = runtime.Context(config(), max_ctx=128)
+    kv = runtime.DeviceKV4(ctx.cfg, 8, 8)
+    kv.reset(ctx)
+    kv.extend(ctx, 1)
+    x = torch.randn(1, 256, device="cuda")
+    y = torch.randn(1, 1024, device="cuda")[:, 512:768]     # one row: its stride says nothing
+    kv.append(ctx, 1, x, y)
+    kv.append(ctx, 1, x[:0], y[:0])
+    k, v = kv.read(ctx, 1, 0, 1)
+    for got, rows in ((k, x), (v, y)):
+        c, b = u.quantise_rows(rows.cpu().numpy(), 2)
+        want = (u.code_values()[c] * u.scale_values()[b].repeat(16, -1)).reshape(1, 256)
+        assert np.array_equal(got.cpu().numpy(), want.astype(np.float32))
+    assert kv.read(ctx, 1, 0, 0)[0].shape == (0, 256)
+    two = torch.randn(2, 512, device="cuda")
+    for bad in ((two[:, :256], torch.randn(2, 256, device="cuda")), (two[:, ::2], two[:, ::2]), (two[:, :256], two[:1, :256])):
+        with pytest.raises(ValueError):
+            kv.append(ctx, 1, *bad)
+    assert abi.spec_last_status(ctx.h) == 0
+    ctx.close()
