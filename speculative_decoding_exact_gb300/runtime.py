@@ -76,6 +76,21 @@ class Context:
             abi.spec_verify_destroy(self.h)
             self.h = None
 
+    def follow(self, *tensors: torch.Tensor):
+        """Work enqueued on the context's stream after this comes after the current
+        stream's so far, and the tensors' memory is kept until it is done."""
+        current = torch.cuda.current_stream()
+        if current.cuda_stream != self.stream.cuda_stream:
+            self.stream.wait_stream(current)
+            for t in tensors:
+                t.record_stream(self.stream)
+
+    def lead(self):
+        """The current stream's work after this comes after the context's so far."""
+        current = torch.cuda.current_stream()
+        if current.cuda_stream != self.stream.cuda_stream:
+            current.wait_stream(self.stream)
+
     def __del__(self):
         try:
             self.close()
@@ -248,7 +263,8 @@ class DeviceKV4(PagedKV):
 
     def append(self, ctx: Context, layer: int, k: torch.Tensor, v: torch.Tensor):
         """Quantise fp32 rows [n][n_kv*dh] (row stride shared by k and v) into
-        the last n positions, which extend() has mapped."""
+        the last n positions, which extend() has mapped.  The context's stream
+        waits for the current one, which wrote the rows."""
         self._check_rows("k", k)
         self._check_rows("v", v)
         n, w = k.shape
@@ -257,15 +273,19 @@ class DeviceKV4(PagedKV):
                              f"{v.shape[0]} by {v.stride(0)}")
         if n == 0:
             return                                          # an empty tensor has no address
+        ctx.follow(k, v)
         abi.check("spec_kv4_append", abi.spec_kv4_append(ctx.h, self.struct(), layer, ptr(k), ptr(v),
                                                          k.stride(0) if n > 1 else w, n))
 
     def read(self, ctx: Context, layer: int, pos0: int, n: int):
-        """fp32 (k, v) rows [n][n_kv*dh] of positions pos0 .. pos0+n-1."""
+        """fp32 (k, v) rows [n][n_kv*dh] of positions pos0 .. pos0+n-1, for use on the
+        current stream (which waits for the context's)."""
         if n < 0:
             raise ValueError(f"n: at least 0 rows, not {n}")
         w = self.cfg.n_kv_heads * self.cfg.head_dim
         k, v = torch.empty((n, w), device="cuda"), torch.empty((n, w), device="cuda")
+        ctx.follow(k, v)
         if n > 0:
             abi.check("spec_kv4_read", abi.spec_kv4_read(ctx.h, self.struct(), layer, pos0, n, ptr(k), ptr(v), w))
+        ctx.lead()
         return k, v

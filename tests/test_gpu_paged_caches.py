@@ -141,6 +141,40 @@ def test_a_4bit_cache_beside_sliding_window_layers():
     ctx.close()
 
 
+def test_append_and_read_of_rows_on_another_stream():
+    """Rows written on the current stream, a context on a stream of its own, results
+    used on the current stream at once: every call waits for what it needs."""
+    own = torch.cuda.Stream()
+    ctx = runtime.Context(config(), max_ctx=128, stream=own)
+    kv = runtime.DeviceKV4(ctx.cfg, 8, 8)
+    sync()
+    kv.reset(ctx)
+    kv.extend(ctx, 100)
+    sync()
+    rng = np.random.default_rng(1)
+    for i in range(3):
+        rows = rng.standard_normal((100, 512)).astype(np.float32)
+        src = torch.from_numpy(rows).cuda()
+        sync()
+        x = torch.zeros(100, 512, device="cuda")
+        torch.cuda._sleep(20_000_000)                       # some 10 ms: x is written late
+        x.copy_(src)
+        kv.append(ctx, 1, x[:, :256], x[:, 256:])
+        del x
+        junk = torch.full((100, 512), 7.0, device="cuda")   # may take x's memory
+        with torch.cuda.stream(own):
+            torch.cuda._sleep(20_000_000)                   # k and v are written late
+        k, v = kv.read(ctx, 1, 0, 100)
+        got = torch.cat((k, v), 1).clone()
+        sync()
+        want = np.concatenate([(u.code_values()[c] * u.scale_values()[b].repeat(16, -1)).reshape(100, 256)
+                               for c, b in (u.quantise_rows(rows[:, j * 256:j * 256 + 256], 2) for j in range(2))], 1)
+        assert np.array_equal(got.cpu().numpy(), want.astype(np.float32)), i
+        del junk
+    assert abi.spec_last_status(ctx.h) == 0
+    ctx.close()
+
+
 def test_append_of_single_rows_and_other_strides():
     ctx = runtime.Context(config(), max_ctx=128)
     kv = runtime.DeviceKV4(ctx.cfg, 8, 8)
