@@ -576,7 +576,14 @@ cudaError_t launch_paged_attention(bool k4, const KvView& kv, int layer, const f
     const long long ws = ((long long)window + 14 + kKeys - 1) / kKeys + 1;       // tiles of window + 15 keys
     const long long ss = ((long long)sinks + kKeys - 1) / kKeys;
     long long L = (ws + ss) / pl.C > 1 ? (ws + ss) / pl.C : 1;
-    while ((ss + L - 1) / L + (ws + L - 2) / L + 1 > pl.C) ++L;
+    // bisected: a window without an end (2^31 - 1) would take millions of steps
+    for (long long most = ws + ss; L < most;) {
+      const long long mid = (L + most) / 2;
+      if ((ss + mid - 1) / mid + (ws + mid - 2) / mid + 1 > pl.C)
+        L = mid + 1;
+      else
+        most = mid;
+    }
     pl.Lw = (int)(L < INT32_MAX ? L : INT32_MAX);
     if (pl.Lw == 1 && ss + ws < pl.slots) pl.slots = (int)(ss + ws);
   }

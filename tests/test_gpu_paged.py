@@ -7,6 +7,8 @@ One-hot rows: where the largest score leads by more than 2^8 (base 2) and more t
 the products' rounding, every other weight is 0 in fp32 and the row's output is
 that key's V row, off by the roundings of one product, one sum and one quotient.
 """
+import time
+
 import numpy as np
 import pytest
 
@@ -211,4 +213,29 @@ def test_infinite_v_elements_reach_the_rows_that_see_them_alike(nq, M, window, s
             assert np.array_equal(part, got[i:i + m], equal_nan=True), (spot, i, m)
         kv.seq_len[0] = length
         kv.pool.copy_(saved)
+    assert status(ctx) == 0
+
+
+# ---------------------------------------------------------------------------
+# the plan of the chunks
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_window_without_an_end_is_planned_at_once(kind):
+    """Windows and sinks of 2^31 - 1 (no limit): the result without a window, and no
+    search of millions of steps on the host (73 ms a call with four chunks)."""
+    ctx = context(64, 64)
+    kv, _, _, _ = cache(ctx, kind, 600, 13)
+    q = np.random.default_rng(5).standard_normal((2, 64, 128)).astype(np.float32)
+    want = attend(ctx, kv, kind, q, 0, 0)
+    most = 2 ** 31 - 1
+    for window, sinks in ((most, 0), (most, most), (600, most)):
+        assert same_bits(attend(ctx, kv, kind, q, window, sinks), want)
+    qd, out, st = torch.from_numpy(q).cuda(), torch.empty(2, 64 * 128, device="cuda"), kv.struct()
+    f = abi.spec_attention_kv4 if kind == "kv4" else abi.spec_attention_window
+    sync()
+    t0 = time.perf_counter()
+    for _ in range(20):
+        abi.check("attention", f(ctx.h, st, 1, qd.data_ptr(), 2, most, most, out.data_ptr()))
+    assert time.perf_counter() - t0 < 0.2
+    sync()
     assert status(ctx) == 0
