@@ -18,6 +18,7 @@ torch = pytest.importorskip("torch")
 
 from speculative_decoding_exact_gb300 import abi, runtime  # noqa: E402
 from tests import kv4_util as u  # noqa: E402
+from tests import paged_util as pu  # noqa: E402
 from tests import test_gpu_kv4 as base  # noqa: E402
 
 EPS = 2.0 ** -24
@@ -238,4 +239,24 @@ def test_a_window_without_an_end_is_planned_at_once(kind):
         abi.check("attention", f(ctx.h, st, 1, qd.data_ptr(), 2, most, most, out.data_ptr()))
     assert time.perf_counter() - t0 < 0.2
     sync()
+    assert status(ctx) == 0
+
+
+# ---------------------------------------------------------------------------
+# precision
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nq,M", [(2, 1), (2, 16), (26, 1), (26, 4), (26, 9), (26, 16)])
+@pytest.mark.parametrize("length", [300, 5000, 33000])
+def test_accuracy(kind, nq, M, length):
+    """Every kernel (few rows, one tile, two tiles) and every part of its operands: far
+    below what a lost part would cost."""
+    ctx = context(nq, 2, max_ctx=40000)
+    kv, k, v, _ = cache(ctx, kind, length, 53)
+    q = np.random.default_rng(11).standard_normal((M, nq, 128)).astype(np.float32)
+    got = attend(ctx, kv, kind, q, 0, 0)
+    want = pu.attention64(q, k, v, nq, 0, 0, length)[0]
+    err = pu.rel_l2(got, want)
+    print(f"{kind} {nq} heads, {M} rows, {length} keys: {err:.2e}")
+    assert err < pu.ACCURACY
     assert status(ctx) == 0
