@@ -242,6 +242,50 @@ def test_a_window_without_an_end_is_planned_at_once(kind):
     assert status(ctx) == 0
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nq,M", [(64, 4), (128, 16)])
+@pytest.mark.parametrize("window,sinks", [(600, 0), (600, 300), (1000, 128), (2000, 5), (700, 2000)])
+def test_windows_that_limit_the_chunks(kind, nq, M, window, sinks):
+    """Few chunks (64 KV heads: four), lengths around every step of the chunks' length
+    and far behind the last: chunks of several tiles for sinks and window, chunks that
+    hold both, blocks on both sides of a step."""
+    ctx = context(nq, 64)
+    longest = 3000
+    kv, k, v, _ = cache(ctx, kind, longest, 43)
+    q = np.random.default_rng(5).standard_normal((M, nq, 128)).astype(np.float32)
+    for length in (512 + M // 2, 1024, 1024 + M // 2, 1536 + M, 2048 + M // 2, 2049, longest):
+        kv.seq_len[0] = length
+        whole = attend(ctx, kv, kind, q, window, sinks)
+        want, bound = pu.attention64(q, k, v, nq, window, sinks, length, split=base.SPLIT[kind])
+        assert (np.abs(whole - want) <= bound).all(), length
+        assert pu.rel_l2(whole, want) < pu.ACCURACY, length
+        for i, m in ((M - 1, 1), (M // 2, M - M // 2)) if nq < 128 else ((7, 9), (3, 11), (0, 10)):
+            kv.seq_len[0] = length - M + i + m
+            assert same_bits(attend(ctx, kv, kind, q[i:i + m], window, sinks), whole[i:i + m]), (length, i, m)
+    assert status(ctx) == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (6000, 300), (3000, 5000)])
+def test_two_row_tiles_across_a_step(kind, window, sinks):
+    """16 rows of 13 heads on each of two KV heads, 38 chunks: around the position where
+    chunks become two tiles long."""
+    nq, M = 26, 16
+    ctx = context(nq, 2, max_ctx=40000)
+    kv, k, v, _ = cache(ctx, kind, 9800, 47)
+    q = np.random.default_rng(5).standard_normal((M, nq, 128)).astype(np.float32)
+    for length in (38 * 128 + 9, 2 * 38 * 128 + 5, 9800):
+        kv.seq_len[0] = length
+        whole = attend(ctx, kv, kind, q, window, sinks)
+        want, bound = pu.attention64(q, k, v, nq, window, sinks, length, split=base.SPLIT[kind])
+        assert (np.abs(whole - want) <= bound).all(), length
+        assert pu.rel_l2(whole, want) < pu.ACCURACY, length
+        for i, m in ((6, 10), (1, 12), (4, 11)):
+            kv.seq_len[0] = length - M + i + m
+            assert same_bits(attend(ctx, kv, kind, q[i:i + m], window, sinks), whole[i:i + m]), (length, i, m)
+    assert status(ctx) == 0
+
+
 # ---------------------------------------------------------------------------
 # precision
 # ---------------------------------------------------------------------------
