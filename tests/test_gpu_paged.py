@@ -304,3 +304,103 @@ def test_accuracy(kind, nq, M, length):
     print(f"{kind} {nq} heads, {M} rows, {length} keys: {err:.2e}")
     assert err < pu.ACCURACY
     assert status(ctx) == 0
+
+
+# ---------------------------------------------------------------------------
+# calls that follow each other
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("nq,M", [(2, 1), (2, 3), (26, 1), (26, 9), (26, 16)])
+def test_4bit_calls_next_to_each_other(nq, M):
+    """No other launch between the calls, so that each may start while the one before
+    ends: append and attention over its rows, append and read, norm with rotation and
+    attention with its q (one row: q is the row's first columns), attention with the
+    output before as q.  The same bits as with a pause after every call."""
+    ctx = context(nq, 2, max_ctx=1024, rope_theta=1e4)
+    rounds, n, length = 24, 200, 700
+    kv, _, _, _ = cache(ctx, "kv4", length, 5)
+    start = kv.pool.clone()
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    rows = torch.randn(rounds, 2, n, 512, generator=gen, device="cuda")
+    q = torch.randn(rounds, M, nq * 128, generator=gen, device="cuda")
+    x = torch.randn(rounds, M, (nq + 2) * 128, generator=gen, device="cuda")
+    pos = torch.arange(length - M, length, dtype=torch.int32, device="cuda")
+    # two views of the cache: the pages in two orders
+    tables = [kv.page_table.clone(), torch.cat((torch.flip(kv.page_table[:length // 16], (0,)), kv.page_table[length // 16:]))]
+    views = [kv.struct() for _ in tables]
+    for s, t in zip(views, tables):
+        s.page_table = t.data_ptr()
+    h, p = ctx.h, lambda t: t.data_ptr()
+
+    def run(pause):
+        kv.pool.copy_(start)
+        held = torch.zeros(rounds, 2, n, 512, device="cuda")
+        qk = torch.zeros_like(x)
+        out = torch.zeros(rounds, 4, M, nq * 128, device="cuda")
+        sync()
+
+        def call(name, *args):
+            abi.check(name, getattr(abi, name)(h, *args))
+            if pause:
+                sync()
+        for i in range(rounds):
+            st = views[i % 2]
+            a, b, r, s = p(rows[i, 0]), p(rows[i, 1]), p(held[i, 0]), p(held[i, 1])
+            call("spec_kv4_append", st, 1, a, a + 1024, 512, n)
+            call("spec_attention_kv4", st, 1, p(q[i]), M, 300, 7, p(out[i, 0]))
+            call("spec_attention_kv4", st, 1, p(out[i, 0]), M, 0, 0, p(out[i, 1]))
+            call("spec_kv4_read", st, 1, length - n, n, r, r + 1024, 512)
+            call("spec_kv4_append", st, 1, b, b + 1024, 512, n)
+            call("spec_kv4_read", st, 1, length - n, n, s, s + 1024, 512)
+            call("spec_qk_norm_rope", p(x[i]), x.shape[2], M, p(pos), None, None, p(qk[i]), x.shape[2])
+            # (for more rows than one, M rows of nq heads are what lies there)
+            call("spec_attention_kv4", st, 1, p(qk[i]), M, 64, 0, p(out[i, 2]))
+            call("spec_attention_kv4", views[1 - i % 2], 1, p(out[i, 2]), M, 300, 7, p(out[i, 3]))
+        sync()
+        return held, qk, out
+    want = run(True)
+    assert all(torch.isfinite(t).all() and t.abs().max() > 0 for t in want)
+    for _ in range(3):
+        got = run(False)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert status(ctx) == 0
+
+
+@pytest.mark.parametrize("nq,M", [(2, 1), (2, 3), (26, 1), (26, 9), (26, 16)])
+def test_bf16_calls_next_to_each_other(nq, M):
+    """Attention whose q is the output of the call before, over two orders of the pages,
+    and after norm with rotation."""
+    ctx = context(nq, 2, max_ctx=1024, rope_theta=1e4)
+    rounds, length = 30, 700
+    kv, _, _, _ = cache(ctx, "bf16", length, 5)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(rounds, M, (nq + 2) * 128, generator=gen, device="cuda")
+    pos = torch.arange(length - M, length, dtype=torch.int32, device="cuda")
+    tables = [kv.page_table.clone(), torch.cat((torch.flip(kv.page_table[:length // 16], (0,)), kv.page_table[length // 16:]))]
+    views = [kv.struct() for _ in tables]
+    for s, t in zip(views, tables):
+        s.page_table = t.data_ptr()
+    h, p = ctx.h, lambda t: t.data_ptr()
+
+    def run(pause):
+        qk = torch.zeros_like(x)
+        out = torch.zeros(rounds, 4, M, nq * 128, device="cuda")
+        sync()
+
+        def call(name, *args):
+            abi.check(name, getattr(abi, name)(h, *args))
+            if pause:
+                sync()
+        for i in range(rounds):
+            call("spec_qk_norm_rope", p(x[i]), x.shape[2], M, p(pos), None, None, p(qk[i]), x.shape[2])
+            src = qk[i]
+            for j, (window, sinks) in enumerate(((0, 0), (300, 7), (64, 0), (0, 0))):
+                call("spec_attention_window", views[(i + j) % 2], 1, p(src), M, window, sinks, p(out[i, j]))
+                src = out[i, j]
+        sync()
+        return qk, out
+    want = run(True)
+    assert all(torch.isfinite(t).all() and t.abs().max() > 0 for t in want)
+    for _ in range(3):
+        got = run(False)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert status(ctx) == 0
