@@ -437,10 +437,9 @@ pattn_kernel(const float* __restrict__ q, PattnPlan pl, KvView kv, int layer, fl
 // mod 4; a warp takes 32 neighbouring rows, which lie side by side in the
 // partials.  With m the largest chunk maximum (base 2) and w_c = 2^(m_c - m):
 //   out = sum_c w_c o_c / sum_c w_c l_c, over the chunks in which the row sees a
-// key, first within each residue in chunk order with a running maximum, then over
-// the residues.  Every step is one of the row's own chunks, so a row's bits do not
-// depend on the block.  (Rescaled once per batch of 8 loads the bits did, where the
-// first row's window started in an earlier chunk.)
+// key: within each residue its largest maximum, then the sums in chunk order, then
+// the same over the residues.  Every step is one of the row's own chunks, so a row's
+// bits do not depend on the block.
 // ---------------------------------------------------------------------------
 constexpr int kMergeParts = 4;
 
@@ -469,11 +468,9 @@ pattn_merge_kernel(const float4* __restrict__ part_o, const float2* __restrict__
   const float4* po = part_o + (size_t)hd * R + r;
   pdl_wait();
   constexpr int kBatch = 8;                             // loads in flight
-  float m = -INFINITY, L = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j0 = 0; j0 < n; j0 += kBatch) {
-    float4 y[kBatch];
-    float2 x[kBatch];
+  float4 y[kBatch];
+  float2 x[kBatch];
+  auto load = [&](int j0) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       x[k] = make_float2(0.f, 0.f);
@@ -483,20 +480,34 @@ pattn_merge_kernel(const float4* __restrict__ part_o, const float2* __restrict__
         y[k] = ldg_now(po + 32 * c * step);
       }
     }
-    // one chunk after the other, in rounded operations that are spelled out: what
-    // depended on the place in the batch would depend on where the block's list starts
+  };
+  load(0);
+  float m = -INFINITY, L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  // the largest maximum of all batches first: sums that were rescaled from batch to
+  // batch would depend on where the block's list starts
+#pragma unroll 4
+  for (int j = kBatch; j < n; ++j) {
+    const float2 z = ldg_now(part_ml + at + (size_t)slot(j) * step);
+    if (z.y != 0.f) m = fmaxf(m, z.x);
+  }
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k)
+    if (x[k].y != 0.f) m = fmaxf(m, x[k].x);
+  for (int j0 = 0;;) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k)
       if (x[k].y != 0.f) {
-        const float up = x[k].x - m, e = exp2_approx(-fabsf(up));      // m = -inf at first: 0
-        const float a = up > 0.f ? e : 1.f, w = up > 0.f ? 1.f : e;
-        m = fmaxf(m, x[k].x);
-        L = fmaf(w, x[k].y, __fmul_rn(L, a));
-        o.x = fmaf(w, y[k].x, __fmul_rn(o.x, a));
-        o.y = fmaf(w, y[k].y, __fmul_rn(o.y, a));
-        o.z = fmaf(w, y[k].z, __fmul_rn(o.z, a));
-        o.w = fmaf(w, y[k].w, __fmul_rn(o.w, a));
+        const float w = exp2_approx(x[k].x - m);
+        L = fmaf(w, x[k].y, L);
+        o.x = fmaf(w, y[k].x, o.x);
+        o.y = fmaf(w, y[k].y, o.y);
+        o.z = fmaf(w, y[k].z, o.z);
+        o.w = fmaf(w, y[k].w, o.w);
       }
+    j0 += kBatch;
+    if (j0 >= n) break;
+    load(j0);
   }
   o_sm[res][lane] = o;
   ml_sm[res][lane] = make_float2(m, L);
