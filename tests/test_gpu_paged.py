@@ -404,3 +404,87 @@ def test_bf16_calls_next_to_each_other(nq, M):
         got = run(False)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert status(ctx) == 0
+
+
+# ---------------------------------------------------------------------------
+# queries that are not finite, and a captured layer
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nq,M", [(2, 4), (2, 16), (26, 9), (26, 16)])
+def test_a_query_that_is_not_finite_spoils_its_own_row(kind, nq, M):
+    ctx = context(nq, 2)
+    kv, _, _, _ = cache(ctx, kind, 900, 61)
+    q = np.random.default_rng(5).standard_normal((M, nq, 128)).astype(np.float32)
+    clean = attend(ctx, kv, kind, q, 0, 0).reshape(M, nq, 128)
+    for val in (np.nan, np.inf, -np.inf):
+        bad = q.copy()
+        bad[1, 0, 77] = bad[M - 1, nq - 1, 0] = val
+        bad[2] = 0                                          # a row of zeros: the mean of V
+        got = attend(ctx, kv, kind, bad, 0, 0).reshape(M, nq, 128)
+        spoilt = np.zeros((M, nq), dtype=bool)
+        spoilt[1, 0] = spoilt[M - 1, nq - 1] = True
+        assert not np.isfinite(got[spoilt]).any()
+        keep = ~spoilt
+        keep[2] = False
+        assert same_bits(got[keep], clean[keep])
+        assert np.isfinite(got[2][~spoilt[2]]).all()
+    assert status(ctx) == 0
+
+
+@pytest.mark.parametrize("nq,M", [(2, 1), (26, 5)])
+def test_a_captured_layer_replayed(nq, M):
+    """Norm with rotation, extend, append, attention and read, captured on a stream of
+    their own and replayed with new inputs: the bits of eager calls."""
+    nkv, length, steps = 2, 400, 4
+    cfg = base.config(nq, nkv, rope_theta=1e4)
+    width = (nq + 2 * nkv) * 128
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    xs = torch.randn(steps, M, width, generator=gen, device="cuda")
+    qs = torch.randn(steps, M, nq * 128, generator=gen, device="cuda")
+    prompt = torch.randn(length, 2 * nkv * 128, generator=gen, device="cuda")
+    sync()
+
+    def run(captured):
+        stream = torch.cuda.Stream()
+        results = []
+        with torch.cuda.stream(stream):
+            ctx = runtime.Context(cfg, max_ctx=1024, stream=stream)
+            kv = runtime.DeviceKV4(cfg, 64, 64)
+            kv.reset(ctx)
+            kv.extend(ctx, length)
+            kv.append(ctx, 1, prompt[:, :nkv * 128], prompt[:, nkv * 128:])
+            x, q = torch.zeros(M, width, device="cuda"), torch.zeros(M, nq * 128, device="cuda")
+            pos = torch.zeros(M, dtype=torch.int32, device="cuda")
+            out, back = torch.zeros(M, nq * 128, device="cuda"), torch.zeros(2, length, nkv * 128, device="cuda")
+            st, h, p = kv.struct(), ctx.h, lambda t: t.data_ptr()
+            k, v = p(x) + 4 * nq * 128, p(x) + 4 * (nq + nkv) * 128
+
+            def layer():
+                abi.check("qk", abi.spec_qk_norm_rope(h, p(x), width, M, p(pos), None, None, p(x), width))
+                abi.check("extend", abi.spec_kv_extend(h, st, M))
+                abi.check("append", abi.spec_kv4_append(h, st, 1, k, v, width, M))
+                abi.check("attention", abi.spec_attention_kv4(h, st, 1, p(q), M, 300, 5, p(out)))
+                abi.check("read", abi.spec_kv4_read(h, st, 1, 20, length, p(back[0]), p(back[1]), nkv * 128))
+            graph = None
+            for i in range(steps):
+                x.copy_(xs[i])
+                q.copy_(qs[i])
+                pos.copy_(torch.arange(length + i * M, length + (i + 1) * M, dtype=torch.int32))
+                if not captured:
+                    layer()
+                else:
+                    if graph is None:
+                        stream.synchronize()
+                        graph = torch.cuda.CUDAGraph()
+                        with torch.cuda.graph(graph, stream=stream):
+                            layer()
+                    graph.replay()
+                stream.synchronize()
+                results.append((x.clone(), out.clone(), back.clone(), int(kv.seq_len[0])))
+            stream.synchronize()
+            assert status(ctx) == 0
+            ctx.close()
+        return results
+    for a, b in zip(run(False), run(True)):
+        assert a[3] == b[3] and all(torch.equal(s, t) for s, t in zip(a[:3], b[:3]))
+        assert all(torch.isfinite(t).all() and t.abs().max() > 0 for t in a[:3])
