@@ -114,7 +114,10 @@ extern "C" {
  * Q = H; a draft block may differ, e.g. 48 query heads at H = 6656);
  * n_q_heads is a multiple of n_kv_heads, at most 13 query heads per KV head;
  * head_dim = 128; page_size = 16; max_rows <= 16 (k_max + 1).  max_ctx
- * bounds the attention workspace (positions per sequence). */
+ * bounds the workspace of the steps' attention (positions per sequence); that of
+ * spec_attention_window and spec_attention_kv4 does not depend on it: max(4, SMs
+ * / n_kv_heads) * n_q_heads * 8,320 bytes, 16 MB for 52 heads on 4, in the same
+ * memory. */
 typedef struct spec_config {
     int32_t hidden;       /* H, e.g. 6656                                   */
     int32_t n_layers;     /* e.g. 52                                        */
@@ -442,6 +445,8 @@ SPEC_API int spec_attention(spec_ctx* ctx, const spec_kv* kv, int layer,
  * layer that is a sliding-window layer of the ctx keeps its K/V in a ring, not
  * in the pool, and is refused (SPEC_EINVAL).  A bounded device wait that gives
  * up sets SPEC_ST_DEVICE_WAIT in the ctx status word, and out is incomplete.
+ * The partial sums lie in the ctx's workspace: calls of one ctx, or graphs
+ * captured from them, must not run at the same time.
  * q DEVICE fp32 [M][n_q_heads][head_dim]; out DEVICE fp32
  * [M][n_q_heads*head_dim]; both 16-byte aligned, not overlapping. */
 SPEC_API int spec_attention_window(spec_ctx* ctx, const spec_kv* kv, int layer, const float* q, int M,

@@ -29,16 +29,19 @@
 // 192 KB and more per tile, 208 rows over 32k keys took 100 us when this layout
 // took 57.
 //
-// What bounds it: 32 MMAs of 128 x 128 x 16 take 2,600 cycles a tile, the softmax
-// and the unpacking 8,400 warp instructions (2,100 cycles of four schedulers at
-// best, half of the slots are used): 3,200 cycles a tile.  A call of one tile per
+// What bounds it: 32 MMAs of 128 x 128 x 16 take 2,600 cycles a tile, 8,750 warp
+// instructions, most of them softmax and unpacking, 2,190 cycles of four schedulers
+// at best (half of the slots are used): 3,200 cycles a tile.  A call of one tile per
 // CTA is latency: 3,000 cycles to the sequence length and the plan, 4,700 to page
 // ids, pages and the unpacked K, 3,900 for the tile, 2,500 to store.  16 rows of 52
-// heads on 4: 11.5 us behind 2k keys, 34.2 behind 32k (408 TFLOP/s, counting each
-// product once; two parts make it two).
+// heads on 4: 11.5 us behind 2k keys, 34.1 behind 32k (410 TFLOP/s, counting each
+// product once; two parts make it two).  Both row tiles of a KV head unpack every
+// page, each in its own CTA.  128 bytes a thread are spilled.
 //
 // Precision: all operands are binary16.  A 4-bit value is exact in it; q and p are
-// split into two parts, 22 significant bits.  The tensor core truncates its
+// split into two parts, 22 significant bits.  q is first multiplied by log2(e) /
+// sqrt(d), rounded once, so that the scores come in base-2 units times a power of two
+// and the largest less itself is exactly 0.  The tensor core truncates its
 // additions, so the small parts go first, and each tile's O starts afresh and is
 // added up in fp32 registers: left in TMEM over 27 tiles it was off by 8e-6.
 #include "attn_mma.cuh"

@@ -6,16 +6,19 @@
 // row, each tile's O added in registers, a chunk of L tiles per CTA.
 //
 // K and V pages are operands as they are: TMA lays them down swizzled, and no
-// thread touches K.  Q and P go in three bf16 parts by truncation, 24 bits, so
-// nothing is rounded and no value is out of range.  Binary16 operands (two parts)
+// thread touches K.  Q and P go in three bf16 parts by truncation, 24 bits, so no
+// value is out of range and nothing is rounded but q's product with log2(e) /
+// sqrt(d), once.  Binary16 operands (two parts)
 // took conversions of every page and a second path for elements past binary16;
 // 104 rows over 32k keys took 48 us with them when this took 39 (now 35).
 //
 // What bounds it: the MMAs.  A 128 x 128 x 16 product takes 121 cycles with both
 // operands in shared memory (Q . K^T) and 81 with one in TMEM (P . V), 48 of them
-// 4,850 cycles a tile; the tile's 64 KB come in 2,850 at the SM's share of HBM.  The
-// TMEM has no room for more than one of Q's parts beside S, P and O.  16 rows of 52
-// heads on 4 with a window of 4096: 16.4 us, most of it latency of two tiles.
+// 4,850 cycles a tile; the tile's 64 KB come in 2,850 at the SM's share of HBM.  O, S
+// and P take 448 of the 512 columns of the TMEM: one of Q's three parts would fit in
+// the rest and save 8 x 40 cycles a tile (not tried).  140 bytes a thread are
+// spilled.  16 rows of 52 heads on 4 with a window of 4096: 16.4 us, of which the
+// MMAs of a CTA's two tiles are 4.7; 8 rows and a window of 32768: 35.2.
 //
 // 0 * NaN is NaN, so an element of V that is not finite would reach rows that do
 // not see its key.  Four warps look through each V tile before its MMAs; such

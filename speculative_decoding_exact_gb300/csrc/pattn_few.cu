@@ -15,12 +15,12 @@
 // What bounds it: the dependent steps of a few warps.  A 4-bit page is 520 warp
 // instructions, 64 of them MMAs of 8 cycles; two warps per scheduler fill 42 % of the
 // slots, 2,300 cycles a tile against 800 at the SM's share of HBM.  One token of 52
-// heads on 4 behind 128k keys: 41 us in 4 bits, 61 in bf16; 8.1 us behind 2k keys, of
-// which the join is 3.  (12 warps of 168 registers: 40 and 60 us, but 8.7 behind 2k
-// keys, and 10.4 instead of 9.4 for a bf16 window of 1024.  One 4-bit page at a time:
-// 5 % slower.  Pages loaded into registers in fragment order: 52 when this took 43.
-// Keys on the 128 rows of tcgen05 MMAs and query rows as columns: 42, with twice the
-// code.)
+// heads on 4 behind 128k keys: 40.3 us in 4 bits, 59.7 in bf16; 7.8 us behind 2k keys,
+// 8.5 for a bf16 window of 1024.  (An earlier build took 41, 61, 8.1, of which the
+// join was 3, and 9.4; with 12 warps of 168 registers 40, 60, 8.7 and 10.4.  One
+// 4-bit page at a time: 5 % slower.  Pages loaded into registers in fragment order: 52
+// when this took 43.  Keys on the 128 rows of tcgen05 MMAs and query rows as columns:
+// 42, with twice the code.)
 //
 // The d's of a K row and the d's and keys of a V page may be visited in any
 // order.  Lane 4n + g (g < 4) takes d's 32 g .. of K (one 16-byte chunk of codes, 64

@@ -11,7 +11,7 @@
 //
 // Bound by memory traffic, 8 bytes per element.  All of a warp's loads are in
 // flight at once, 4 KB: 8191 rows of 56 heads take 72 us, 6.6 TB/s (a warp per
-// head, 512 bytes in flight: 108); one row 4.1 us, a launch.
+// head, 512 bytes in flight: 108); one row 4.3 us, a launch.
 #include "common.cuh"
 #include "internal.h"
 
